@@ -662,6 +662,7 @@ const char* sparsepr_status_string(sparsepr_status s) {
     case SPARSEPR_ERR_CUDA: return "CUDA error";
     case SPARSEPR_ERR_TIMEOUT: return "device wait limit reached";
     case SPARSEPR_ERR_NUMERIC: return "numerical error (empty kept set or non-finite value)";
+    case SPARSEPR_ERR_CAPACITY: return "no free page, or a table row too short";
   }
   return "unknown status";
 }

@@ -302,6 +302,59 @@ cudaError_t launch_correct(const float* o_sparse, const float* od, const int32_t
                            const int32_t* perm_q, const float* bp32, const float* bv32, int H,
                            int N, int n_corr, int M, int d, void* out, bool out_bf16,
                            cudaStream_t st);
+
+// ---- window.cu: attention with a window of frames ---------------------------
+struct WindowArgs {
+  const void *q, *k, *v;
+  void* out;
+  float* lse;  // may be null
+  const int32_t *n_q, *n_k;  // [B], may be null
+  int B, Hq, Hkv, Nq, Nk, d;
+  sparsepr_visibility see;
+  float sc;  // scale * log2(e)
+  bool bf16;
+  DeviceStats* stats;
+};
+cudaError_t launch_window_attention(const WindowArgs& a, cudaStream_t st);
+
+// ---- cache.cu: the paged 8-bit cache ----------------------------------------
+struct CacheArgs {
+  sparsepr_cache_params p;
+  sparsepr_cache c;
+  DeviceStats* stats;
+  // scratch in the workspace
+  int32_t* counts;   // [16]
+  int32_t* pages;    // [n_pages] free pages (reserve), pages that move (compact)
+  int32_t* targets;  // [n_pages] where they go (compact)
+  int32_t* remap;    // [n_pages] (compact)
+  int32_t* copies;   // [2, B] source and target of the copied last pages (reserve)
+  int sm_count;
+};
+cudaError_t launch_cache_reserve(const CacheArgs& a, const int32_t* n_new, int32_t* start,
+                                 cudaStream_t st);
+cudaError_t launch_cache_append(const CacheArgs& a, const void* k, const void* v, bool bf16, int T,
+                                const int32_t* start, const int32_t* n_new, cudaStream_t st);
+cudaError_t launch_cache_fork(const CacheArgs& a, const int32_t* src, const int32_t* dst, int n,
+                              cudaStream_t st);
+cudaError_t launch_cache_free(const CacheArgs& a, const int32_t* seq, int n, cudaStream_t st);
+cudaError_t launch_cache_evict(const CacheArgs& a, const sparsepr_visibility& see,
+                               cudaStream_t st);
+cudaError_t launch_cache_compact(const CacheArgs& a, int32_t* n_used, cudaStream_t st);
+
+// ---- cache_attn.cu: attention over the cache --------------------------------
+struct CacheAttnArgs {
+  CacheArgs cache;
+  const void* q;
+  void* out;
+  float* lse;          // may be null
+  const int32_t* n_q;  // may be null
+  int Hq, Nq;
+  sparsepr_visibility see;
+  float sc;  // scale * log2(e)
+  bool bf16;
+};
+cudaError_t launch_cache_attention(const CacheAttnArgs& a, cudaStream_t st);
+
 cudaError_t launch_pairs_exec(const int64_t* pairs_sparse, int H, int64_t add, int64_t* pairs_exec,
                               DeviceStats* stats, cudaStream_t st);
 

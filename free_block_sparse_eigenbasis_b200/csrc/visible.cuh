@@ -1,0 +1,136 @@
+// Visibility by frames (sparsepr_visibility) and the attention of one row
+// taken literally, shared by the windowed attention and the attention over
+// the cache.
+#pragma once
+
+#include "common.cuh"
+
+namespace spr {
+
+constexpr float kLog2eF = 1.4426950408889634f;
+constexpr float kLn2F = 0.6931471805599453f;
+
+// Visible keys of a query: [0, s) and [lo, hi), disjoint, s <= lo <= hi <= L.
+struct Range {
+  int s, lo, hi;
+};
+
+// Keys that the query at position p of a sequence of L keys sees. All three
+// ends grow with p, so the keys of a run of rows lie in [0, s of the last row)
+// and [lo of the first, hi of the last).
+__host__ __device__ inline Range visible_range(const sparsepr_visibility& see, long long p,
+                                               long long L) {
+  Range r = {0, 0, 0};
+  if (p < 0 || L <= 0) return r;
+  const long long F = see.frame, f = p / F;
+  long long end = L;  // keys a causal query may look at
+  if (see.causal && (f + 1) * F < L) end = (f + 1) * F;
+  long long s = see.sinks * F;
+  if (s > end) s = end;
+  long long lo = 0, hi = end;
+  if (see.window > 0) {
+    lo = (f - see.window + 1) * F;
+    if (lo < 0) lo = 0;
+    if (!see.causal && (f + see.window) * F < L) hi = (f + see.window) * F;
+  }
+  if (lo < s) lo = s;
+  if (hi < lo) hi = lo;
+  r.s = static_cast<int>(s);
+  r.lo = static_cast<int>(lo < L ? lo : L);
+  r.hi = static_cast<int>(hi);
+  if (r.hi < r.lo) r.hi = r.lo;
+  return r;
+}
+
+// In-use rows of one sequence, clamped to what the buffers hold.
+__device__ __forceinline__ int clamp_count(const int32_t* n, int b, int cap, int otherwise,
+                                           DeviceStats* stats, bool report) {
+  if (!n) return otherwise;
+  const int v = n[b];
+  if (report && (v < 0 || v > cap)) raise_status(stats, SPARSEPR_ERR_INVALID_ARG);
+  return min(max(v, 0), cap);
+}
+
+__device__ __forceinline__ float load_f32(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+__device__ __forceinline__ float load_f32(const float* p) { return *p; }
+__device__ __forceinline__ void store_f32(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void store_f32(float* p, float v) { *p = v; }
+
+// One query row by the definition, by all NT threads of a block: a pass over
+// its visible keys with a running maximum and sum, fp32 products, no key
+// outside [0, s) and [lo, hi) touched. It is the reading of rows that meet
+// NaN or infinities (a product with a hidden NaN is NaN even at weight 0).
+//   kv.ok(j)      key j can be read
+//   kv.dot(j, q)  q . k_j            kv.v(j, c)  v_j[c]
+// Returns the maximum m (log2 units, sc = scale * log2 e), the sum l and, in
+// thread c < D, the unnormalised output o of column c; l is NaN for a row whose
+// visible logits are all -inf, and 0 for a row that sees nothing.
+template <int NT>
+struct LiteralScratch {
+  float p[NT];
+  float o[NT];
+  float red[32];
+};
+
+template <int NT, int D, class KV>
+__device__ void literal_row(const KV& kv, const float* q, const Range r, float sc,
+                            LiteralScratch<NT>& sm, float& m_out, float& l_out, float& o_out) {
+  constexpr int kGroups = NT / D;
+  static_assert(kGroups >= 1 && NT % 32 == 0, "threads");
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int total = r.s + (r.hi - r.lo);
+  float m = -INFINITY, l = 0.f, o = 0.f;
+  bool seen = false;
+  const int c = tid % D, grp = tid / D;
+  for (int base = 0; base < total; base += NT) {
+    const int t = base + tid;
+    bool on = false;
+    float x = -INFINITY;
+    if (t < total) {
+      const int j = t < r.s ? t : r.lo + (t - r.s);
+      on = kv.ok(j);
+      if (on) x = sc * kv.dot(j, q);
+    }
+    float mx = on ? x : -INFINITY;
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+    if (lane == 0) sm.red[warp] = mx;
+    seen = __syncthreads_or(on) || seen;
+    for (int w = 0; w < NT / 32; ++w) mx = fmaxf(mx, sm.red[w]);
+    const float mn = fmaxf(m, mx);
+    const float corr = (m == -INFINITY) ? 0.f : exp2f(m - mn);
+    // weight of this thread's key; -1 marks a key that is not there
+    float p = -1.f;
+    if (on) p = (mn == -INFINITY) ? (x == x ? 0.f : x) : exp2f(x - mn);
+    sm.p[tid] = p;
+    __syncthreads();
+    float sum = 0.f;
+    const int n = min(NT, total - base);
+    for (int i = 0; i < n; ++i) {  // the same order in every thread
+      const float w = sm.p[i];
+      if (!(w < 0.f)) sum += w;
+    }
+    l = l * corr + sum;
+    o *= corr;
+    if (grp < kGroups)
+      for (int i = grp; i < n; i += kGroups) {
+        const float w = sm.p[i];
+        if (w < 0.f) continue;
+        const int u = base + i;
+        o += w * kv.v(u < r.s ? u : r.lo + (u - r.s), c);
+      }
+    m = mn;
+    __syncthreads();
+  }
+  sm.o[tid] = o;
+  __syncthreads();
+  if (tid < D)
+    for (int g = 1; g < kGroups; ++g) o += sm.o[g * D + tid];
+  if (seen && l == 0.f) l = __int_as_float(0x7fc00000);
+  __syncthreads();
+  m_out = m;
+  l_out = l;
+  o_out = o;
+}
+
+}  // namespace spr

@@ -17,6 +17,7 @@ _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libsparsep
 MAX_HEADS = 256
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, ERR_TIMEOUT, ERR_NUMERIC = range(7)
+ERR_CAPACITY = 7
 BF16, F32 = 0, 1
 # sparsepr_params.partition; the parameter dicts name the mode as the oracle does
 PARTITION_MODES = dict(response=0, semantic=1, coclustering=2)
@@ -27,7 +28,11 @@ EXPORTED = ("sparsepr_workspace_bytes", "sparsepr_status_string", "sparsepr_part
             "sparsepr_reset_stats", "sparsepr_check_wait_limit", "sparsepr_route_noalloc",
             "sparsepr_workspace_region", "sparsepr_probe_diagnostics",
             "sparsepr_support_expansion", "sparsepr_density_profile", "sparsepr_attention",
-            "sparsepr_check_reciprocal")
+            "sparsepr_check_reciprocal", "sparsepr_window_workspace_bytes",
+            "sparsepr_window_attention", "sparsepr_cache_workspace_bytes",
+            "sparsepr_cache_reserve", "sparsepr_cache_append", "sparsepr_cache_attention",
+            "sparsepr_cache_fork", "sparsepr_cache_free", "sparsepr_cache_evict",
+            "sparsepr_cache_compact")
 
 
 class Params(ctypes.Structure):
@@ -54,6 +59,31 @@ class Stats(ctypes.Structure):
                 ("pairs_exec", ctypes.c_int64 * MAX_HEADS),
                 ("recheck_rows", ctypes.c_int64 * 2),
                 ("eig_sweeps", ctypes.c_int32 * 2), ("near_ties", ctypes.c_int64 * 2)]
+
+
+class Visibility(ctypes.Structure):
+    """sparsepr_visibility: which keys a query sees, by frames."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("frame", "window", "sinks", "causal")]
+
+
+class WindowParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "Hq", "Hkv", "Nq", "Nk", "d")] + [
+        ("see", Visibility), ("scale", ctypes.c_double)]
+
+
+class CacheParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "Hkv", "d", "page", "n_pages", "max_pages")]
+
+
+class CachePointers(ctypes.Structure):
+    """sparsepr_cache: device pointers of a cache."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k8", "v8", "k_scale", "v_scale", "table", "len",
+                                               "ref")]
+
+
+class CacheAttentionParams(ctypes.Structure):
+    _fields_ = [("Hq", ctypes.c_int32), ("Nq", ctypes.c_int32), ("see", Visibility),
+                ("scale", ctypes.c_double)]
 
 
 class SparsePRError(RuntimeError):
@@ -105,6 +135,24 @@ def _load():
     lib.sparsepr_check_wait_limit.argtypes = [V, V]
     lib.sparsepr_check_reciprocal.argtypes = [P, ctypes.c_int64, P, V]
     lib.sparsepr_check_reciprocal.restype = st
+    WP, CP, CC = (ctypes.POINTER(x) for x in (WindowParams, CacheParams, CachePointers))
+    CA, SEE, I32 = ctypes.POINTER(CacheAttentionParams), ctypes.POINTER(Visibility), ctypes.c_int32
+    lib.sparsepr_window_workspace_bytes.argtypes = [WP, st]
+    lib.sparsepr_window_workspace_bytes.restype = sz
+    lib.sparsepr_cache_workspace_bytes.argtypes = [CP, CA]
+    lib.sparsepr_cache_workspace_bytes.restype = sz
+    for name, args in (
+            ("window_attention", [P, P, P, st, WP, I32P, I32P, P, P]),
+            ("cache_reserve", [CP, CC, I32P, I32P]),
+            ("cache_append", [P, P, st, I32, CP, CC, I32P, I32P]),
+            ("cache_attention", [P, st, CP, CC, CA, I32P, P, P]),
+            ("cache_fork", [CP, CC, I32P, I32P, I32]),
+            ("cache_free", [CP, CC, I32P, I32]),
+            ("cache_evict", [CP, CC, SEE]),
+            ("cache_compact", [CP, CC, I32P])):
+        fn = getattr(lib, "sparsepr_" + name)
+        fn.argtypes = args + [V, sz, V]
+        fn.restype = st
     for name in ("sparsepr_partition", "sparsepr_permute", "sparsepr_route",
                  "sparsepr_block_sparse_attn", "sparsepr_probe_correct", "sparsepr_read_stats",
                  "sparsepr_reset_stats", "sparsepr_check_wait_limit"):
@@ -357,6 +405,202 @@ def sparsepr_check_reciprocal(x, stream=None):
     _check(lib.sparsepr_check_reciprocal(x.data_ptr(), x.numel(), err.data_ptr(), _stream(stream)),
            "sparsepr_check_reciprocal")
     return err
+
+
+# ---- windowed attention and the 8-bit cache ---------------------------------
+
+F8 = torch.float8_e4m3fn
+
+
+def _visibility(p: dict) -> Visibility:
+    return Visibility(int(p.get("frame", 1)), int(p.get("window", 0)), int(p.get("sinks", 0)),
+                      int(p.get("causal", 1)))
+
+
+def make_window_params(p: dict) -> WindowParams:
+    """ctypes parameters of the windowed attention from a plain dict (B, Hq,
+    Hkv, Nq, Nk, d; frame, window, sinks, causal as in sparsepr_visibility,
+    by default token-causal without a window; scale)."""
+    return WindowParams(int(p["B"]), int(p["Hq"]), int(p["Hkv"]), int(p["Nq"]), int(p["Nk"]),
+                        int(p["d"]), _visibility(p), float(p.get("scale", 0.0)))
+
+
+def make_cache_params(p: dict) -> CacheParams:
+    return CacheParams(int(p["B"]), int(p["Hkv"]), int(p["d"]), int(p["page"]), int(p["n_pages"]),
+                       int(p["max_pages"]))
+
+
+def make_cache_attention_params(a: dict) -> CacheAttentionParams:
+    return CacheAttentionParams(int(a["Hq"]), int(a["Nq"]), _visibility(a),
+                                float(a.get("scale", 0.0)))
+
+
+@dataclass
+class Cache:
+    """A paged cache of keys and values in e4m3 (see include/sparsepr.h), all
+    tensors owned by torch."""
+    k8: torch.Tensor       # [n_pages, Hkv, page, d] float8_e4m3fn
+    v8: torch.Tensor
+    k_scale: torch.Tensor  # [n_pages, Hkv] fp32
+    v_scale: torch.Tensor
+    table: torch.Tensor    # [B, max_pages] int32, -1 = no page
+    len: torch.Tensor      # [B] int32
+    ref: torch.Tensor      # [n_pages] int32
+
+
+def allocate_cache(p: dict, device="cuda") -> Cache:
+    """An empty cache."""
+    if int(lib.sparsepr_cache_workspace_bytes(ctypes.byref(make_cache_params(p)), None)) == 0:
+        raise SparsePRError(ERR_INVALID_ARG, "allocate_cache")
+    pages, shape = (int(p["n_pages"]), int(p["Hkv"])), (int(p["page"]), int(p["d"]))
+    i32 = dict(dtype=torch.int32, device=device)
+    return Cache(
+        k8=torch.zeros(pages + shape, dtype=torch.uint8, device=device).view(F8),
+        v8=torch.zeros(pages + shape, dtype=torch.uint8, device=device).view(F8),
+        k_scale=torch.ones(pages, dtype=torch.float32, device=device),
+        v_scale=torch.ones(pages, dtype=torch.float32, device=device),
+        table=torch.full((int(p["B"]), int(p["max_pages"])), -1, **i32),
+        len=torch.zeros(int(p["B"]), **i32), ref=torch.zeros(int(p["n_pages"]), **i32))
+
+
+def _cleared_workspace(nbytes: int, where: str, device) -> torch.Tensor:
+    if nbytes == 0:
+        raise SparsePRError(ERR_INVALID_ARG, where)
+    return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+
+
+def allocate_window_workspace(p: dict, dtype: torch.dtype, device="cuda") -> torch.Tensor:
+    """Workspace of sparsepr_window_attention with a clear status word."""
+    prm = make_window_params(p)
+    return _cleared_workspace(int(lib.sparsepr_window_workspace_bytes(
+        ctypes.byref(prm), _DTYPE_CODES.get(dtype, -1))), "window_workspace_bytes", device)
+
+
+def allocate_cache_workspace(p: dict, attn: Optional[dict] = None, device="cuda") -> torch.Tensor:
+    """Workspace of the cache calls (with attn: of that attention too) with a
+    clear status word."""
+    prm = make_cache_params(p)
+    a = None if attn is None else ctypes.byref(make_cache_attention_params(attn))
+    return _cleared_workspace(int(lib.sparsepr_cache_workspace_bytes(ctypes.byref(prm), a)),
+                              "cache_workspace_bytes", device)
+
+
+_DTYPE_CODES = {torch.bfloat16: BF16, torch.float32: F32}
+
+
+def _opt(t, name, shape, dtype):
+    return None if t is None else _arg(t, name, shape, dtype)
+
+
+def _call(where: str, fn, tensors, args, ws, stream):
+    """One library call on the device of its tensors and, unless a stream is
+    given, on that device's current stream."""
+    wp, wb = _ws(ws)
+    dev = ws.device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError("%s: all tensors must be on one device" % where)
+    if dev.type != "cuda" or dev.index == torch.cuda.current_device():
+        _check(fn(*args, wp, wb, _stream(stream)), where)
+        return
+    with torch.cuda.device(dev):
+        _check(fn(*args, wp, wb, _stream(stream)), where)
+
+
+def sparsepr_window_attention(q, k, v, p: dict, out, ws, lse=None, n_q=None, n_k=None,
+                              stream=None):
+    """Attention with a sliding window of frames and sink frames: q, out
+    [B, Hq, Nq, d], k, v [B, Hkv, Nk, d] bf16 or fp32; lse [B, Hq, Nq] fp32,
+    n_q and n_k [B] int32, each optional (see include/sparsepr.h)."""
+    prm = make_window_params(p)
+    B, Hq, Hkv, Nq, Nk, d = prm.B, prm.Hq, prm.Hkv, prm.Nq, prm.Nk, prm.d
+    dt = _dtype_code(q)
+    _call("sparsepr_window_attention", lib.sparsepr_window_attention,
+          (q, k, v, out, lse, n_q, n_k),
+          (_arg(q, "q", (B, Hq, Nq, d)), _arg(k, "k", (B, Hkv, Nk, d), q.dtype),
+           _arg(v, "v", (B, Hkv, Nk, d), q.dtype), dt, ctypes.byref(prm),
+           _opt(n_q, "n_q", (B,), I32), _opt(n_k, "n_k", (B,), I32),
+           _arg(out, "out", (B, Hq, Nq, d), q.dtype),
+           _opt(lse, "lse", (B, Hq, Nq), torch.float32)), ws, stream)
+
+
+def _cache(p: dict, c: Cache):
+    prm = make_cache_params(p)
+    pages, f32 = (prm.n_pages, prm.Hkv), torch.float32
+    ptr = CachePointers(
+        _arg(c.k8, "k8", pages + (prm.page, prm.d), F8), _arg(c.v8, "v8", pages + (prm.page, prm.d), F8),
+        _arg(c.k_scale, "k_scale", pages, f32), _arg(c.v_scale, "v_scale", pages, f32),
+        _arg(c.table, "table", (prm.B, prm.max_pages), I32), _arg(c.len, "len", (prm.B,), I32),
+        _arg(c.ref, "ref", (prm.n_pages,), I32))
+    return prm, ctypes.byref(prm), ctypes.byref(ptr), (c.k8, c.v8, c.k_scale, c.v_scale, c.table,
+                                                       c.len, c.ref)
+
+
+def sparsepr_cache_reserve(n_new, p: dict, cache: Cache, start, ws, stream=None):
+    """Pages for n_new [B] int32 more tokens per sequence; start [B] int32
+    receives the lengths before (-1 throughout if there is no room)."""
+    prm, pp, cp, ts = _cache(p, cache)
+    _call("sparsepr_cache_reserve", lib.sparsepr_cache_reserve, ts + (n_new, start),
+          (pp, cp, _arg(n_new, "n_new", (prm.B,), I32), _arg(start, "start", (prm.B,), I32)), ws,
+          stream)
+
+
+def sparsepr_cache_append(k, v, p: dict, cache: Cache, start, n_new, ws, stream=None):
+    """Write the tokens k, v [B, Hkv, T, d] (bf16 or fp32; the first n_new[b]
+    of each sequence, all T where n_new is None) at start[b] in 8 bits."""
+    prm, pp, cp, ts = _cache(p, cache)
+    dt = _dtype_code(k)
+    shape = (prm.B, prm.Hkv, k.shape[2] if k.dim() == 4 else -1, prm.d)
+    _call("sparsepr_cache_append", lib.sparsepr_cache_append, ts + (k, v, start, n_new),
+          (_arg(k, "k", shape), _arg(v, "v", shape, k.dtype), dt, shape[2], pp, cp,
+           _arg(start, "start", (prm.B,), I32), _opt(n_new, "n_new", (prm.B,), I32)), ws, stream)
+
+
+def sparsepr_cache_attention(q, p: dict, cache: Cache, attn: dict, out, ws, lse=None, n_q=None,
+                             stream=None):
+    """Attention of q [B, Hq, Nq, d] over the cached tokens; attn: Hq, Nq and
+    the visibility (see include/sparsepr.h)."""
+    prm, pp, cp, ts = _cache(p, cache)
+    a = make_cache_attention_params(attn)
+    shape = (prm.B, a.Hq, a.Nq, prm.d)
+    dt = _dtype_code(q)
+    _call("sparsepr_cache_attention", lib.sparsepr_cache_attention, ts + (q, out, lse, n_q),
+          (_arg(q, "q", shape), dt, pp, cp, ctypes.byref(a), _opt(n_q, "n_q", (prm.B,), I32),
+           _arg(out, "out", shape, q.dtype), _opt(lse, "lse", shape[:3], torch.float32)), ws,
+          stream)
+
+
+def sparsepr_cache_fork(src, dst, p: dict, cache: Cache, ws, stream=None):
+    """Sequence dst[i] becomes a copy of sequence src[i] that shares its pages."""
+    prm, pp, cp, ts = _cache(p, cache)
+    n = src.numel()
+    _call("sparsepr_cache_fork", lib.sparsepr_cache_fork, ts + (src, dst),
+          (pp, cp, _arg(src, "src", (n,), I32), _arg(dst, "dst", (n,), I32), n), ws, stream)
+
+
+def sparsepr_cache_free(seq, p: dict, cache: Cache, ws, stream=None):
+    """Empty the sequences named in seq [n] int32."""
+    prm, pp, cp, ts = _cache(p, cache)
+    n = seq.numel()
+    _call("sparsepr_cache_free", lib.sparsepr_cache_free, ts + (seq,),
+          (pp, cp, _arg(seq, "seq", (n,), I32), n), ws, stream)
+
+
+def sparsepr_cache_evict(see: dict, p: dict, cache: Cache, ws, stream=None):
+    """Give up the pages that no later query with this causal, windowed
+    visibility can see."""
+    prm, pp, cp, ts = _cache(p, cache)
+    v = _visibility(see)
+    _call("sparsepr_cache_evict", lib.sparsepr_cache_evict, ts, (pp, cp, ctypes.byref(v)), ws,
+          stream)
+
+
+def sparsepr_cache_compact(p: dict, cache: Cache, n_used, ws, stream=None):
+    """Move the pages in use to the front of the pool; n_used [1] int32
+    receives their number."""
+    prm, pp, cp, ts = _cache(p, cache)
+    _call("sparsepr_cache_compact", lib.sparsepr_cache_compact, ts + (n_used,),
+          (pp, cp, _arg(n_used, "n_used", (1,), I32)), ws, stream)
 
 
 _REGION_DTYPES = dict(init_k=torch.int32, init_q=torch.int32, zplanes=torch.bfloat16,

@@ -65,7 +65,8 @@ typedef enum {
   SPARSEPR_ERR_WORKSPACE = 3,   /* ws smaller than sparsepr_workspace_bytes() or misaligned */
   SPARSEPR_ERR_CUDA = 4,        /* a CUDA runtime call or launch failed */
   SPARSEPR_ERR_TIMEOUT = 5,     /* device status: a bounded wait ran out */
-  SPARSEPR_ERR_NUMERIC = 6      /* device status: empty kept set or non-finite value */
+  SPARSEPR_ERR_NUMERIC = 6,     /* device status: empty kept set or non-finite value */
+  SPARSEPR_ERR_CAPACITY = 7     /* device status: no free page, or a table row too short */
 } sparsepr_status;
 
 typedef enum { SPARSEPR_BF16 = 0, SPARSEPR_F32 = 1 } sparsepr_dtype;
@@ -395,6 +396,180 @@ sparsepr_status sparsepr_density_profile(const void* q, const void* k, sparsepr_
                                          const sparsepr_params* p, double tau, int32_t row_stride,
                                          double* density, void* ws, size_t ws_bytes,
                                          void* stream);
+
+/* ------------------------------------------------------------------------
+ * Frame-by-frame generation: attention with a window of frames and sink
+ * frames, a paged cache of earlier frames in 8 bits, and attention over it.
+ *
+ * These calls stand beside sparsepr_block_sparse_attn: their sparsity is a
+ * fixed pattern in time instead of a route. They share the conventions at the
+ * top of this file (caller-owned device memory, nothing allocated or
+ * synchronised, argument errors on the host, device-detected errors OR-ed
+ * into the status word at the start of `ws`) except that they keep no
+ * statistics and never clear the status word: call sparsepr_reset_stats(ws)
+ * once before the first call on a workspace. Every call may be captured into a
+ * CUDA graph. Calls that may overlap on the GPU need workspaces of their own.
+ * ------------------------------------------------------------------------ */
+
+/* Which keys a query sees. Tokens are counted in frames of `frame` tokens
+ * (1: single tokens). A query at position p >= 0 and a key at position j < L
+ * of the same sequence lie in frames fq = p / frame and fj = j / frame
+ * (rounded down); the key is visible iff
+ *   (causal == 0 or fj <= fq) and
+ *   (window == 0 or |fq - fj| < window or fj < sinks).
+ * The n queries of a sequence of L keys stand at its end: query i has
+ * p = L - n + i; a query with p < 0 sees nothing. A query that sees nothing
+ * gets the output 0 and the log-sum-exp -inf. Keys and values that a query does
+ * not see have no influence on its output, NaN and infinities included. */
+typedef struct {
+  int32_t frame;  /* tokens per frame, >= 1 */
+  int32_t window; /* frames, 0 = no window */
+  int32_t sinks;  /* leading frames that the window never hides, >= 0 */
+  int32_t causal; /* 0 or 1 */
+} sparsepr_visibility;
+
+typedef struct {
+  int32_t B;    /* sequences */
+  int32_t Hq;   /* query heads, a multiple of Hkv */
+  int32_t Hkv;  /* key / value heads; query head h reads key head h / (Hq / Hkv) */
+  int32_t Nq;   /* query rows per sequence (0 is allowed) */
+  int32_t Nk;   /* key rows per sequence (0 is allowed) */
+  int32_t d;    /* 64 or 128 */
+  sparsepr_visibility see;
+  double scale; /* softmax scale; 0 selects 1/sqrt(d) */
+} sparsepr_window_params;
+
+/* Bytes of workspace of sparsepr_window_attention (0: invalid parameters). */
+size_t sparsepr_window_workspace_bytes(const sparsepr_window_params* p, sparsepr_dtype dt);
+
+/* Windowed attention: out[b, h, i] = sum_j softmax_j(scale q_i . k_j) v_j over
+ * the visible keys j of sequence b.
+ *   q    [B, Hq, Nq, d], k, v [B, Hkv, Nk, d]   dtype dt (device, read only)
+ *   n_q  [B] int32 device or NULL: rows of q in use per sequence (NULL: Nq)
+ *   n_k  [B] int32 device or NULL: rows of k and v in use (NULL: Nk)
+ *   out  [B, Hq, Nq, d] dtype dt, must not overlap q, k, v
+ *   lse  [B, Hq, Nq] fp32 or NULL: natural log of the sum of exponentials
+ * Rows of out and lse behind a sequence's n_q rows are not written; rows of
+ * k and v behind n_k are not used. MMAs in bf16 with fp32 accumulation for
+ * both dtypes (fp32 inputs are rounded to bf16 first), softmax in fp32.
+ * Values of n_q outside [0, Nq] or of n_k outside [0, Nk] raise
+ * SPARSEPR_ERR_INVALID_ARG in the status word and are clamped. */
+sparsepr_status sparsepr_window_attention(const void* q, const void* k, const void* v,
+                                          sparsepr_dtype dt, const sparsepr_window_params* p,
+                                          const int32_t* n_q, const int32_t* n_k, void* out,
+                                          float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* The cache: a pool of pages of `page` tokens. A page holds keys and values of
+ * all Hkv heads as e4m3 (1 sign, 4 exponent, 3 mantissa bits, largest value
+ * 448) with one fp32 scale for each page and head, a power of two: the key it
+ * stands for is k8 * k_scale, exactly representable in bf16. Token t of
+ * sequence b is row t % page of page table[b, t / page]; an entry of -1 holds
+ * no page. ref[x] counts the table entries that name page x, 0 for a free page.
+ * An empty cache has table = -1, len = 0, ref = 0. */
+typedef struct {
+  int32_t B;         /* sequences (table rows), 1..1024 */
+  int32_t Hkv;       /* key / value heads, 1..1024 */
+  int32_t d;         /* 64 or 128 */
+  int32_t page;      /* tokens per page: 16, 32, 64 or 128 */
+  int32_t n_pages;   /* pages of the pool, >= 1 */
+  int32_t max_pages; /* entries of a table row, >= 1; max_pages * page < 2^31 */
+} sparsepr_cache_params;
+
+typedef struct {
+  void* k8;       /* [n_pages, Hkv, page, d] e4m3, 16-byte aligned */
+  void* v8;       /* [n_pages, Hkv, page, d] e4m3, 16-byte aligned */
+  float* k_scale; /* [n_pages, Hkv] */
+  float* v_scale; /* [n_pages, Hkv] */
+  int32_t* table; /* [B, max_pages] */
+  int32_t* len;   /* [B] tokens held */
+  int32_t* ref;   /* [n_pages] */
+} sparsepr_cache;
+
+typedef struct {
+  int32_t Hq;  /* query heads, a multiple of Hkv */
+  int32_t Nq;  /* query rows per sequence (0 is allowed) */
+  sparsepr_visibility see;
+  double scale; /* softmax scale; 0 selects 1/sqrt(d) */
+} sparsepr_cache_attention_params;
+
+/* Bytes of workspace of the cache calls; with `a` NULL of all but
+ * sparsepr_cache_attention (0: invalid parameters). A workspace that serves
+ * an attention serves the other calls too. */
+size_t sparsepr_cache_workspace_bytes(const sparsepr_cache_params* p,
+                                      const sparsepr_cache_attention_params* a);
+
+/* Room for n_new[b] >= 0 more tokens in every sequence: start[b] = len[b], then
+ * len[b] += n_new[b]. New pages are taken from the free ones in ascending
+ * order, for b ascending. A sequence whose partly filled last page is shared
+ * (ref > 1) and that grows gets a copy of that page first (its scales too), as
+ * the first of its new pages; if all that share a page grow in one call, each
+ * gets a copy and the page becomes free.
+ * All or nothing: when the free pages or a table row do not suffice,
+ * SPARSEPR_ERR_CAPACITY is raised; a negative n_new, a len outside the table
+ * or a missing last page raises SPARSEPR_ERR_INVALID_ARG; then the cache stays
+ * as it is and start is -1 throughout (sparsepr_cache_append skips those). */
+sparsepr_status sparsepr_cache_reserve(const sparsepr_cache_params* p, const sparsepr_cache* c,
+                                       const int32_t* n_new, int32_t* start, void* ws,
+                                       size_t ws_bytes, void* stream);
+
+/* Write tokens start[b] .. start[b] + n_new[b] - 1 of every sequence:
+ *   k, v   [B, Hkv, T, d] dtype dt; n_new [B] int32 device or NULL (T each)
+ * Per page and head, the scale is the smallest power of two s >= 2^-110 with
+ * |x| <= 448 s for the new tokens x; if the page holds earlier tokens of the
+ * sequence (start inside the page) it is the larger of that and the page's
+ * scale, and if it grows, the earlier tokens are rounded again to the new scale
+ * (exact but for values that fall below 2^-6 s). Values are rounded to
+ * nearest even; NaN and infinities are stored as NaN and do not enter the
+ * scale. Does not read or change len. start[b] < 0 skips the sequence. An entry
+ * without a page, a page with ref != 1, n_new outside [0, T] or tokens past the
+ * table raise SPARSEPR_ERR_INVALID_ARG and are not written. */
+sparsepr_status sparsepr_cache_append(const void* k, const void* v, sparsepr_dtype dt, int32_t T,
+                                      const sparsepr_cache_params* p, const sparsepr_cache* c,
+                                      const int32_t* start, const int32_t* n_new, void* ws,
+                                      size_t ws_bytes, void* stream);
+
+/* Attention over the cache: sparsepr_window_attention with the keys and
+ * values that the pages of each sequence stand for, L = len[b].
+ *   q [B, Hq, Nq, d] dtype dt, n_q, out, lse as there.
+ * Queries are rounded to 11 significant bits at least, weights likewise, the
+ * softmax and its sums are fp32. A visible token whose table entry holds no
+ * page counts as not visible and raises SPARSEPR_ERR_INVALID_ARG, as do n_q
+ * outside [0, Nq] and len outside the table (clamped). */
+sparsepr_status sparsepr_cache_attention(const void* q, sparsepr_dtype dt,
+                                         const sparsepr_cache_params* p, const sparsepr_cache* c,
+                                         const sparsepr_cache_attention_params* a,
+                                         const int32_t* n_q, void* out, float* lse, void* ws,
+                                         size_t ws_bytes, void* stream);
+
+/* Branch: sequence dst[i] becomes a copy of sequence src[i] that shares all of
+ * its pages (ref + 1 each), i < n. dst[i] has to be empty (len 0), named once
+ * in dst, and in no src; a pair that breaks this or lies outside 0..B-1 raises
+ * SPARSEPR_ERR_INVALID_ARG and is skipped. src, dst: [n] int32 device. */
+sparsepr_status sparsepr_cache_fork(const sparsepr_cache_params* p, const sparsepr_cache* c,
+                                    const int32_t* src, const int32_t* dst, int32_t n, void* ws,
+                                    size_t ws_bytes, void* stream);
+
+/* Empty the n sequences named in seq ([n] int32 device): their entries give up
+ * their pages (ref - 1), table = -1, len = 0. Naming a sequence twice is the
+ * same as once; one outside 0..B-1 raises SPARSEPR_ERR_INVALID_ARG. */
+sparsepr_status sparsepr_cache_free(const sparsepr_cache_params* p, const sparsepr_cache* c,
+                                    const int32_t* seq, int32_t n, void* ws, size_t ws_bytes,
+                                    void* stream);
+
+/* Give up the pages that no later query can see: with a causal visibility,
+ * every page of a sequence whose tokens all lie outside the sink frames and
+ * outside the window of a query at position len[b] (table = -1, ref - 1).
+ * INVALID_ARG for a visibility that is not causal or has no window. */
+sparsepr_status sparsepr_cache_evict(const sparsepr_cache_params* p, const sparsepr_cache* c,
+                                     const sparsepr_visibility* see, void* ws, size_t ws_bytes,
+                                     void* stream);
+
+/* Pack the pool: with n pages in use, the i-th page in use at n or above moves
+ * to the i-th free page below n (both ascending); table and ref follow, so that
+ * the pages in use are 0..n-1. n_used: [1] int32 device, receives n. Bytes of the
+ * pages left behind stay. */
+sparsepr_status sparsepr_cache_compact(const sparsepr_cache_params* p, const sparsepr_cache* c,
+                                       int32_t* n_used, void* ws, size_t ws_bytes, void* stream);
 
 /* Copy the device statistics of the last call out of `ws` (a blocking
  * device-to-host copy; call after the stream has been synchronised). */

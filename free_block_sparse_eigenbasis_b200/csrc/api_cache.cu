@@ -100,10 +100,22 @@ float log2_scale(double scale, int d) {
 }
 
 size_t carve_window(const sparsepr_window_params& p, sparsepr_dtype dt, char* base, WindowArgs* a) {
-  (void)p;
-  (void)dt;
   Carver w{base};
   a->stats = w.take<DeviceStats>(1);
+  const size_t q = static_cast<size_t>(p.B) * p.Hq * p.Nq * p.d;
+  const size_t kv = static_cast<size_t>(p.B) * p.Hkv * p.Nk * p.d;
+  if (dt == SPARSEPR_F32) {
+    a->qb = w.take<__nv_bfloat16>(q);
+    a->kb = w.take<__nv_bfloat16>(kv);
+    a->vb = w.take<__nv_bfloat16>(kv);
+  }
+  if (p.Nq > 0) {
+    const WindowPlan plan = window_plan(p.B, p.Hq, p.Hkv, p.Nq, p.Nk, p.see);
+    const size_t rows = plan.splits > 1
+                            ? static_cast<size_t>(plan.units) * plan.splits * plan.unit_rows : 0;
+    a->opart = w.take<float>(rows * p.d);
+    a->lpart = w.take<float>(rows);
+  }
   return w.at;
 }
 

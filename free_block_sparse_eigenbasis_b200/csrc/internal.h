@@ -314,7 +314,18 @@ struct WindowArgs {
   float sc;  // scale * log2(e)
   bool bf16;
   DeviceStats* stats;
+  // scratch in the workspace
+  __nv_bfloat16 *qb, *kb, *vb;  // fp32 inputs rounded to bf16
+  float *opart, *lpart;         // partial outputs and log2-sum-exps of split key ranges
 };
+struct WindowPlan {
+  int R, segs;    // query rows per segment, segments
+  int unit_rows;  // rows of a unit: 256 or 128
+  int tiles;      // units per segment
+  int units;      // segs * tiles
+  int splits;     // key ranges per unit
+};
+WindowPlan window_plan(int B, int Hq, int Hkv, int Nq, int Nk, const sparsepr_visibility& see);
 cudaError_t launch_window_attention(const WindowArgs& a, cudaStream_t st);
 
 // ---- cache.cu: the paged 8-bit cache ----------------------------------------

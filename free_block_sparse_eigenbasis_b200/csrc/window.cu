@@ -1,4 +1,19 @@
-// Attention with a sliding window of frames and sink frames.
+// Attention with a sliding window of frames and sink frames on the
+// 5th-generation tensor cores.
+//
+// out_i = sum_j p_ij v_j, p_ij = 2^(x_ij - m_i) / l_i, x_ij = scale log2(e) q_i.k_j
+// over the keys that row i sees: [0, s_i) and [lo_i, hi_i), whose ends grow
+// with i. A unit of up to 256 rows of one head therefore needs the keys [0, SA)
+// and [LB, HB) (SA = s of its last row, LB = lo of its first, HB = hi of its
+// last), and nothing between them is read. They are cut into tiles of 128 keys;
+// a tile that every row of a warp sees whole takes no mask.
+//
+// Roles (352 threads) as in the routed attention kernel: two softmax
+// warpgroups (thread = query row = TMEM lane), a warp that streams Q and the
+// K tiles by TMA, one for the V tiles, one thread that issues tcgen05.mma.
+// Units of two 128-row tiles give tile i to warpgroup i; units of one tile give
+// the even key tiles to warpgroup 0 and the odd ones to warpgroup 1, merged at
+// the end. P stays in tensor memory.
 #include "common.cuh"
 #include "internal.h"
 #include "visible.cuh"
@@ -6,59 +21,838 @@
 namespace spr {
 namespace {
 
-constexpr int kRowThreads = 128;
+constexpr int kStages = 2;  // K and V ring depth
+constexpr int kThreads = 352;
+constexpr uint32_t kTmemCols = 512;  // S_0, S_1 (128 columns each), O_0, O_1
+constexpr float kOverflowSum = 4294967296.0f;  // 2^32: a larger half sum moves the reference
+constexpr float kMaxReference = 4194304.0f;
+constexpr int kMaxWindowSplits = 16;
+constexpr int kPlanSMs = 148;
 
-template <typename T, int D>
-struct DenseKV {
-  const T *k, *vals;  // this head's rows
-  __device__ bool ok(int) const { return true; }
-  __device__ float dot(int j, const float* q) const {
-    const T* row = k + static_cast<size_t>(j) * D;
-    float s = 0.f;
-    for (int c = 0; c < D; ++c) s += q[c] * load_f32(row + c);
-    return s;
-  }
-  __device__ float v(int j, int c) const { return load_f32(vals + static_cast<size_t>(j) * D + c); }
+template <int HD>
+struct Smem {
+  static constexpr int kAtoms = HD / 64;          // 128-byte swizzle atoms along d
+  static constexpr int kSlab = kTileM * 128;      // 64 columns of 128 rows (16 KB)
+  static constexpr int kTileBytes = kAtoms * kSlab;
+  static constexpr int q_off = 0;                 // two query tiles
+  static constexpr int k_off = q_off + 2 * kTileBytes;
+  static constexpr int v_off = k_off + kStages * kTileBytes;
+  static constexpr int bar_off = v_off + kStages * kTileBytes;
+  static constexpr int ml_off = bar_off + 256;    // [2][2][128] row maxima and sums
+  static constexpr int flag_off = ml_off + 2048;  // [8] rows for the literal pass
+  static constexpr int bytes = flag_off + 32;
+};
+// The d = 128 footprint for both head dims, so that one block runs per
+// multiprocessor (each takes all 512 columns of tensor memory); the tiles start
+// at a 1024-byte boundary.
+constexpr int kSmemBytes = Smem<128>::bytes + 1024;
+static_assert(kSmemBytes <= static_cast<int>(kMaxDynSmem), "shared memory");
+
+struct Bars {
+  uint64_t q_full;
+  uint64_t kfull[kStages], vfull[kStages], kempty[kStages], vempty[kStages];
+  uint64_t vfix[2];
+  uint64_t s_full[2], p_full[2], o_done[2];
+  uint64_t mma_idle;
+  uint32_t tmem_base;
+  int abort;
+};
+static_assert(sizeof(Bars) <= 256, "barrier block");
+
+struct WindowMaps {
+  CUtensorMap q, k, v;
 };
 
-// One block per query row.
-template <typename T, int D>
-__global__ void __launch_bounds__(kRowThreads) window_rows_kernel(const WindowArgs a) {
-  __shared__ LiteralScratch<kRowThreads> sm;
-  __shared__ float q[D];
-  const int i = blockIdx.x, bh = blockIdx.y, b = bh / a.Hq, h = bh % a.Hq;
-  const bool report = i == 0 && h == 0 && threadIdx.x == 0;
+struct WindowKernelParams {
+  WindowArgs a;
+  int group;           // query heads per key head
+  int R, segs;         // rows per segment, segments (heads, or key heads with packed groups)
+  int tiles;           // units per segment
+  int unit_rows;       // 256 or 128
+  int splits;
+  int q_box_rows, kv_box_rows;
+  float* opart;        // [units, splits, unit_rows, d] normalised partial outputs
+  float* lpart;        // [units, splits, unit_rows] their log2-sum-exps
+};
+
+__device__ __forceinline__ void fma2(float& x0, float& x1, float a0, float a1, float b, float c) {
+  asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %4};\n\tmov.b64 rc, {%5, %5};\n\t"
+      "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(x0), "=f"(x1)
+      : "f"(a0), "f"(a1), "f"(b), "f"(c));
+}
+__device__ __forceinline__ void add2(float2& x, float a, float b) {
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(x.x), "=f"(x.y)
+      : "f"(x.x), "f"(x.y), "f"(a), "f"(b));
+}
+__device__ __forceinline__ float max3f(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                            int32_t x, int32_t y, int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+// bits [a, b) of a 32-bit word (any a, b)
+__device__ __forceinline__ uint32_t bit_range(int a, int b) {
+  a = max(a, 0);
+  b = min(b, 32);
+  if (a >= b) return 0u;
+  return (b == 32 ? 0xFFFFFFFFu : ((1u << b) - 1u)) & ~((1u << a) - 1u);
+}
+
+// The keys of a unit and this block's share of their tiles.
+struct UnitKeys {
+  int SA, LB, HB, TA;  // [0, SA) in TA tiles, then [LB, HB)
+  int j0, T;           // this block's tiles
+  __device__ int start(int j) const { return j < TA ? j * kTileN : LB + (j - TA) * kTileN; }
+  __device__ int end(int j) const {
+    return min(start(j) + kTileN, j < TA ? SA : HB);
+  }
+  __device__ int tile_of(int key) const {
+    return key < SA ? key / kTileN : TA + (key - LB) / kTileN;
+  }
+};
+
+// K and V rows of one head for the literal pass, limited to the block's tiles
+template <int HD>
+struct TileKV {
+  const __nv_bfloat16 *k, *vals;
+  UnitKeys u;
+  __device__ bool ok(int j) const {
+    const int t = u.tile_of(j);
+    return t >= u.j0 && t < u.j0 + u.T;
+  }
+  __device__ float dot(int j, const float* q) const {
+    const uint4* row = reinterpret_cast<const uint4*>(k + static_cast<size_t>(j) * HD);
+    float s = 0.f;
+    for (int c = 0; c < HD / 8; ++c) {
+      const uint4 x = row[c];
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s = fmaf(q[c * 8 + 2 * e], __uint_as_float(w[e] << 16), s);
+        s = fmaf(q[c * 8 + 2 * e + 1], __uint_as_float(w[e] & 0xFFFF0000u), s);
+      }
+    }
+    return s;
+  }
+  __device__ float v(int j, int c) const {
+    return load_f32(vals + static_cast<size_t>(j) * HD + c);
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ void store_row32(T* dst, const uint32_t (&o)[32], float f);
+template <>
+__device__ __forceinline__ void store_row32<float>(float* dst, const uint32_t (&o)[32], float f) {
+#pragma unroll
+  for (int k = 0; k < 32; k += 4)
+    *reinterpret_cast<float4*>(dst + k) =
+        make_float4(__uint_as_float(o[k]) * f, __uint_as_float(o[k + 1]) * f,
+                    __uint_as_float(o[k + 2]) * f, __uint_as_float(o[k + 3]) * f);
+}
+template <>
+__device__ __forceinline__ void store_row32<__nv_bfloat16>(__nv_bfloat16* dst,
+                                                           const uint32_t (&o)[32], float f) {
+#pragma unroll
+  for (int k = 0; k < 32; k += 8) {
+    uint4 u;
+    u.x = pack_bf16x2(__uint_as_float(o[k]) * f, __uint_as_float(o[k + 1]) * f);
+    u.y = pack_bf16x2(__uint_as_float(o[k + 2]) * f, __uint_as_float(o[k + 3]) * f);
+    u.z = pack_bf16x2(__uint_as_float(o[k + 4]) * f, __uint_as_float(o[k + 5]) * f);
+    u.w = pack_bf16x2(__uint_as_float(o[k + 6]) * f, __uint_as_float(o[k + 7]) * f);
+    *reinterpret_cast<uint4*>(dst + k) = u;
+  }
+}
+
+// T: the output type; the inputs are bf16.
+template <int HD, typename T>
+__global__ void __launch_bounds__(kThreads, 1)
+    window_attn_kernel(const __grid_constant__ WindowMaps maps, const WindowKernelParams p) {
+  using L = Smem<HD>;
+  constexpr int kAtoms = HD / 64;
+  const WindowArgs& a = p.a;
+  // block = (unit, split); segments vary fastest, and with a causal visibility the
+  // last rows of all segments, which see the most, come first
+  int bid = blockIdx.x;
+  const int split = bid % p.splits;
+  bid /= p.splits;
+  const int seg = bid % p.segs;
+  int tile = bid / p.segs;
+  if (a.see.causal) tile = p.tiles - 1 - tile;
+  const int unit = seg * p.tiles + tile;
+  const bool packed = p.R != a.Nq;  // the rows of all query heads of a key head
+  const int bh0 = packed ? seg * p.group : seg;  // first (sequence, query head) of the segment
+  const int b = bh0 / a.Hq;
+  const int kvh = b * a.Hkv + (bh0 % a.Hq) / p.group;
+  const bool report = split == 0 && tile == 0 && bh0 % a.Hq == 0 && threadIdx.x == 0;
   const int n = clamp_count(a.n_q, b, a.Nq, a.Nq, a.stats, report);
-  const int L = clamp_count(a.n_k, b, a.Nk, a.Nk, a.stats, report);
-  if (i >= n) return;
-  const size_t row = static_cast<size_t>(bh) * a.Nq + i;
-  for (int c = threadIdx.x; c < D; c += kRowThreads)
-    q[c] = load_f32(static_cast<const T*>(a.q) + row * D + c);
+  const int len = clamp_count(a.n_k, b, a.Nk, a.Nk, a.stats, report);
+  const int r0 = tile * p.unit_rows;
+  const int rows_unit = min(p.unit_rows, p.R - r0);
+  const int nq = rows_unit > kTileM ? 2 : 1;
+  const size_t row_base = static_cast<size_t>(bh0) * a.Nq + r0;  // of q, out, lse
+  // first and last query of the unit (packed rows wrap from head to head)
+  int i_first = r0 % a.Nq, i_last = (r0 + rows_unit - 1) % a.Nq;
+  if (r0 / a.Nq != (r0 + rows_unit - 1) / a.Nq) {
+    i_first = 0;
+    i_last = a.Nq - 1;
+  }
+  if (i_first >= n) return;  // every row lies behind the sequence
+  i_last = min(i_last, n - 1);
+  const long long pos0 = static_cast<long long>(len) - n;  // position of query 0
+  UnitKeys u;
+  {
+    const Range first = visible_range(a.see, max(pos0 + i_first, 0ll), len);
+    const Range last = visible_range(a.see, pos0 + i_last, len);
+    u.SA = last.s;
+    u.LB = first.lo;
+    u.HB = last.hi;
+    if (u.LB <= u.SA) {  // one range
+      u.SA = 0;
+      u.LB = 0;
+    }
+    u.HB = max(u.HB, u.LB);
+  }
+  u.TA = (u.SA + kTileN - 1) / kTileN;
+  const int T_all = u.TA + (u.HB - u.LB + kTileN - 1) / kTileN;
+  u.j0 = static_cast<int>(static_cast<long long>(T_all) * split / p.splits);
+  u.T = static_cast<int>(static_cast<long long>(T_all) * (split + 1) / p.splits) - u.j0;
+  const int T_tiles = u.T, j0 = u.j0;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool partial = p.splits > 1;
+  const size_t pbase = (static_cast<size_t>(unit) * p.splits + split) * p.unit_rows;
+  T* const out = static_cast<T*>(a.out);
+
+  if (T_tiles == 0) {
+    for (int r = threadIdx.x; r < rows_unit; r += kThreads) {
+      if (partial) {
+        p.lpart[pbase + r] = -INFINITY;
+      } else if ((r0 + r) % a.Nq < n) {
+        for (int c = 0; c < HD; c += 16 / static_cast<int>(sizeof(T)))
+          *reinterpret_cast<uint4*>(out + (row_base + r) * HD + c) = make_uint4(0, 0, 0, 0);
+        if (a.lse) a.lse[row_base + r] = -INFINITY;
+      }
+    }
+    return;
+  }
+  // tasks of warpgroup i: two query tiles -> every key tile; one -> tiles 2t + i
+  const bool two = nq == 2;
+  const int ntask[2] = {two ? T_tiles : (T_tiles + 1) / 2, two ? T_tiles : T_tiles / 2};
+  // A tile that ends behind the sequence holds rows of V that may be anything,
+  // also NaN, and a weight of 0 does not silence them: the V warp clears them.
+  // (Rows behind the buffer are zero already: TMA fills them.) At most the last
+  // tile of each key range is such a tile.
+  auto needs_fix = [&](int j) {
+    return u.start(j) + kTileN > len && (len < a.Nk || p.kv_box_rows < kTileN);
+  };
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* Qs = smem + L::q_off;
+  uint8_t* Ks = smem + L::k_off;
+  uint8_t* Vs = smem + L::v_off;
+  Bars* bars = reinterpret_cast<Bars*>(smem + L::bar_off);
+  float* ml = reinterpret_cast<float*>(smem + L::ml_off);
+  uint32_t* flags = reinterpret_cast<uint32_t*>(smem + L::flag_off);
+
+  if (threadIdx.x == 0) {
+    mbar_init(&bars->q_full, 1);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&bars->kfull[s], 1);
+      mbar_init(&bars->vfull[s], 1);
+      mbar_init(&bars->kempty[s], 1);
+      mbar_init(&bars->vempty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->vfix[i], 1);
+      mbar_init(&bars->s_full[i], 1);
+      mbar_init(&bars->p_full[i], kTileM);
+      mbar_init(&bars->o_done[i], 1);
+    }
+    mbar_init(&bars->mma_idle, 1);
+    bars->abort = 0;
+    fence_barrier_init();
+  }
+  if (threadIdx.x < 8) flags[threadIdx.x] = 0;
+  if (warp == 0) {
+    tmem_alloc(&bars->tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
   __syncthreads();
-  const size_t base = (static_cast<size_t>(b) * a.Hkv + h / (a.Hq / a.Hkv)) * a.Nk * D;
-  const DenseKV<T, D> kv = {static_cast<const T*>(a.k) + base, static_cast<const T*>(a.v) + base};
-  float m, l, o;
-  literal_row<kRowThreads, D>(kv, q, visible_range(a.see, static_cast<long long>(L) - n + i, L),
-                              a.sc, sm, m, l, o);
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  for (int c = threadIdx.x; c < D; c += kRowThreads)
-    store_f32(static_cast<T*>(a.out) + row * D + c, o * inv);
-  if (a.lse && threadIdx.x == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2F;
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  volatile int* abort = &bars->abort;
+
+  if (warp == 8 || warp == 10) {
+    // ------- TMA producers: warp 8 Q and the K tiles, warp 10 the V tiles ------
+    const bool is_k = warp == 8;
+    uint8_t* ring = is_k ? Ks : Vs;
+    uint64_t* full = is_k ? bars->kfull : bars->vfull;
+    uint64_t* empty = is_k ? bars->kempty : bars->vempty;
+    const CUtensorMap* map = is_k ? &maps.k : &maps.v;
+    const uint32_t bytes = kAtoms * p.kv_box_rows * 128;
+    if (is_k && lane == 0) {
+      mbar_arrive_expect_tx(&bars->q_full, nq * kAtoms * p.q_box_rows * 128);
+      for (int qt = 0; qt < nq; ++qt)
+        for (int c = 0; c < kAtoms; ++c)
+          tma_load_2d(Qs + qt * L::kTileBytes + c * L::kSlab, &maps.q, &bars->q_full, c * 64,
+                      static_cast<int32_t>(row_base) + qt * kTileM);
+    }
+    int issued = -1, fixes = 0;
+    for (int j = 0; j < T_tiles; ++j) {
+      const int st = j % kStages, k0 = u.start(j0 + j);
+      bool ok = true;
+      if (lane == 0) {
+        if (j >= kStages) ok = mbar_wait(&empty[st], ((j / kStages) + 1) & 1, abort);
+        if (ok) {
+          mbar_arrive_expect_tx(&full[st], bytes);
+          for (int c = 0; c < kAtoms; ++c)
+            tma_load_3d(ring + st * L::kTileBytes + c * L::kSlab, map, &full[st], c * 64, k0, kvh);
+        }
+      }
+      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+      issued = j;
+      if (!is_k && needs_fix(j0 + j)) {
+        ok = mbar_wait(&full[st], (j / kStages) & 1, abort);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        for (int c = 0; c < kAtoms; ++c)
+          for (int x = (len - k0) * 8 + lane; x < kTileN * 8; x += 32)
+            *reinterpret_cast<uint4*>(ring + st * L::kTileBytes + c * L::kSlab + x * 16) =
+                make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->vfix[fixes]);
+        ++fixes;
+      }
+    }
+    // let the loads already in flight land before the block goes on
+    if (lane == 0) {
+      volatile int never = 0;
+      for (int j = max(0, issued - kStages + 1); j <= issued; ++j)
+        mbar_wait(&full[j % kStages], (j / kStages) & 1, &never);
+      if (is_k) mbar_wait(&bars->q_full, 0, &never);
+    }
+  } else if (warp == 9) {
+    // ------------------------------ MMA issuer --------------------------------
+    if (lane == 0) {
+      constexpr uint32_t idS = idesc_bf16(kTileM, kTileN, 0);
+      constexpr uint32_t idO = idesc_bf16(kTileM, HD, 1);
+      const uint32_t q_addr = smem_u32(Qs), k_addr = smem_u32(Ks), v_addr = smem_u32(Vs);
+      bool ok = mbar_wait(&bars->q_full, 0, abort);
+      auto kv_of = [&](int i, int t) { return two ? t : 2 * t + i; };
+      // S_i = Q_(tile of i) K(kv)^T
+      auto issue_s = [&](int i, int t) -> bool {
+        const int kv = kv_of(i, t), st = kv % kStages;
+        if (!mbar_wait(&bars->kfull[st], (kv / kStages) & 1, abort)) return false;
+        tc_fence_after();
+        const uint32_t qa = q_addr + (two ? i : 0) * L::kTileBytes;
+        const uint32_t d_tmem = tmem + static_cast<uint32_t>(i * kTileN);
+#pragma unroll
+        for (int ks = 0; ks < HD / 16; ++ks) {
+          const uint32_t off = static_cast<uint32_t>((ks >> 2) * L::kSlab + (ks & 3) * 32);
+          mma_bf16_ss(d_tmem, smem_desc_sw128(qa + off, 16, 1024),
+                      smem_desc_sw128(k_addr + st * L::kTileBytes + off, 16, 1024), idS,
+                      ks > 0 ? 1u : 0u);
+        }
+        mma_commit(&bars->s_full[i]);
+        if (!two || i == 1) mma_commit(&bars->kempty[st]);  // last reader of K(kv)
+        return true;
+      };
+      // O_i += P_i V(kv), P_i from tensor memory
+      int fixes = 0, fix_of = -1;
+      auto issue_pv = [&](int i, int t) -> bool {
+        const int kv = kv_of(i, t), st = kv % kStages;
+        if (!mbar_wait(&bars->p_full[i], t & 1, abort)) return false;
+        if (!mbar_wait(&bars->vfull[st], (kv / kStages) & 1, abort)) return false;
+        if (kv != fix_of && needs_fix(j0 + kv)) {
+          if (!mbar_wait(&bars->vfix[fixes], 0, abort)) return false;
+          fix_of = kv;
+          ++fixes;
+        }
+        tc_fence_after();
+        const uint32_t o_tmem = tmem + 2u * kTileN + static_cast<uint32_t>(i * HD);
+        const uint32_t p_tmem = tmem + static_cast<uint32_t>(i * kTileN);
+#pragma unroll
+        for (int ks = 0; ks < kTileN / 16; ++ks)
+          mma_bf16_ts(o_tmem, p_tmem + static_cast<uint32_t>(ks * 8),
+                      smem_desc_sw128(v_addr + st * L::kTileBytes + ks * 16 * 128, L::kSlab, 1024),
+                      idO, (t > 0 || ks > 0) ? 1u : 0u);
+        if (!two || i == 1) mma_commit(&bars->vempty[st]);  // last reader of V(kv)
+        if (t == ntask[i] - 1) mma_commit(&bars->o_done[i]);
+        return true;
+      };
+      for (int i = 0; i < 2 && ok; ++i)
+        if (ntask[i] > 0) ok = issue_s(i, 0);
+      const int nt = max(ntask[0], ntask[1]);
+      for (int t = 0; t < nt && ok; ++t)
+        for (int i = 0; i < 2 && ok; ++i) {
+          if (t >= ntask[i]) continue;
+          ok = issue_pv(i, t);
+          if (ok && t + 1 < ntask[i]) ok = issue_s(i, t + 1);
+        }
+      // all issued MMAs complete before the block releases tensor memory
+      mma_commit(&bars->mma_idle);
+      volatile int never = 0;
+      mbar_wait(&bars->mma_idle, 0, &never);
+    }
+  } else {
+    // ------------- softmax: warpgroup i = warp / 4, thread = row -------------
+    const int i = warp >> 2;
+    const int row = (warp & 3) * 32 + lane;  // 0..127 == TMEM lane
+    const int ur = two ? i * kTileM + row : row;  // row of the unit
+    const uint32_t lane_base = static_cast<uint32_t>(((warp & 3) * 32) << 16);
+    const uint32_t s_tmem = tmem + lane_base + static_cast<uint32_t>(i * kTileN);
+    const uint32_t o_base = tmem + lane_base + 2u * kTileN;
+    const float sc = a.sc;
+    const int qi = (r0 + ur) % a.Nq;
+    const bool valid = ur < rows_unit && qi < n;
+    Range rg = {0, 0, 0};
+    if (valid) rg = visible_range(a.see, pos0 + qi, len);
+    // rows that nobody reads, and rows that see nothing, take every key unmasked
+    // against the reference 0 and are dropped at the end
+    const bool live = valid && (rg.s > 0 || rg.hi > rg.lo);
+    float m_ref = live ? -INFINITY : 0.f, l_sum = 0.f;
+    bool ok = true, seen = false;
+    for (int t = 0; t < ntask[i]; ++t) {
+      const int kv = two ? t : 2 * t + i;  // local key tile
+      const int k0 = u.start(j0 + kv), k1 = u.end(j0 + kv);
+      const bool whole = !live || (k1 == k0 + kTileN && (k1 <= rg.s || (rg.lo <= k0 && k1 <= rg.hi) ||
+                                                         (rg.s == rg.lo && k1 <= rg.hi)));
+      const bool masked = !__all_sync(0xffffffffu, whole);
+      uint32_t km[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
+      if (masked && !whole) {
+        const int e = min(rg.s, k1) - k0, lo = rg.lo - k0, hi = min(rg.hi, k1) - k0;
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+          km[w] = bit_range(-32 * w, e - 32 * w) | bit_range(lo - 32 * w, hi - 32 * w);
+      }
+      seen = seen || (km[0] | km[1] | km[2] | km[3]) != 0u;
+      // tcgen05.ld / st below are warp-collective: the warp proceeds or stops as one
+      if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[i], t & 1, abort))) { ok = false; break; }
+      tc_fence_after();
+      // The row is processed in two halves of 64 key columns: S half hf is
+      // loaded, exponentiated and packed, and its P stored over columns
+      // [32 hf, 32 hf + 32) of S_i, columns that hold S values already read.
+      uint32_t r[kTileN / 2];
+      auto load_half = [&](int hf) {
+        tmem_ld32(s_tmem + hf * 64, *reinterpret_cast<uint32_t(*)[32]>(r));
+        tmem_ld32(s_tmem + hf * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(r + 32));
+        tmem_wait_ld();
+        if (masked) {
+#pragma unroll
+          for (int c = 0; c < kTileN / 2; ++c)
+            if (!((km[2 * hf + (c >> 5)] >> (c & 31)) & 1u)) r[c] = __float_as_uint(-INFINITY);
+        }
+      };
+      // scaled maximum of the loaded half: eight chains of three-input maxima
+      auto half_max = [&]() -> float {
+        float m8[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) m8[k] = __uint_as_float(r[k]);
+#pragma unroll
+        for (int c = 8; c < kTileN / 2; c += 2)
+          m8[(c >> 1) & 7] = max3f(m8[(c >> 1) & 7], __uint_as_float(r[c]), __uint_as_float(r[c + 1]));
+        return sc * fmaxf(max3f(m8[0], m8[1], m8[2]),
+                          fmaxf(max3f(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7])));
+      };
+      // P = 2^(s sc - m_ref) of the loaded half as bf16 pairs; returns its sum
+      uint32_t pk[32];
+      auto exp_half = [&](float mref) -> float {
+        float2 r4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                        make_float2(0.f, 0.f)};
+        const float nm = (mref == -INFINITY) ? 0.f : -mref;  // no visible key yet: P = 0
+#pragma unroll
+        for (int c = 0; c < kTileN / 2; c += 2) {
+          float xa, xb;
+          fma2(xa, xb, __uint_as_float(r[c]), __uint_as_float(r[c + 1]), sc, nm);
+          const float ea = ex2_approx(xa), eb = ex2_approx(xb);
+          add2(r4[(c >> 1) & 3], ea, eb);
+          pk[c >> 1] = pack_bf16x2(ea, eb);
+        }
+        return (r4[0].x + r4[0].y + r4[1].x + r4[1].y) + (r4[2].x + r4[2].y + r4[3].x + r4[3].y);
+      };
+      // Reference maximum m_ref: the row maximum of the first tile that holds
+      // one of the row's keys, rounded up to a whole number (so that a move by k
+      // below is exact; a reference of 2^22 and more goes to the literal pass);
+      // later tiles are exponentiated against it with no
+      // maximum pass. A half whose sum exceeds 2^32 moves the reference up by
+      // the whole number k of log2 units that brings its largest value to at
+      // most 1: its values are formed again, and the P half already stored,
+      // the row sum and O are scaled by 2^-k, exactly. O and the row sum
+      // always share one reference, so the result is exact.
+      if (__any_sync(0xffffffffu, m_ref == -INFINITY)) {
+        load_half(0);
+        const float m0 = half_max();
+        load_half(1);
+        const float mt = fmaxf(m0, half_max());
+        if (m_ref == -INFINITY) m_ref = ceilf(mt);
+      }
+      float alpha = 1.f, rs = 0.f;
+      bool need = false;
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        load_half(hf);
+        float rh = exp_half(m_ref);
+        const bool over = live && rh > kOverflowSum;  // NaN goes to the literal pass
+        if (__any_sync(0xffffffffu, over)) {
+          load_half(hf);
+          float sh = 1.f;  // 2^-k, formed from its bits (0 when k >= 127)
+          if (over) {
+            const float k = fminf(ceilf(half_max() - m_ref), 16384.f);
+            sh = (k < 127.f) ? __int_as_float((127 - static_cast<int>(k)) << 23) : 0.f;
+            m_ref += k;
+            need = true;
+          }
+          alpha *= sh;
+          rs *= sh;
+          if (hf == 1 && __any_sync(0xffffffffu, sh != 1.f)) {
+            // the stored P half 0 follows the new reference (exact: a power of two)
+            uint32_t q[32];
+            tmem_ld32(s_tmem, q);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              q[c] = pack_bf16x2(__uint_as_float(q[c] << 16) * sh,
+                                 __uint_as_float(q[c] & 0xFFFF0000u) * sh);
+            tmem_st32(s_tmem, q);
+          }
+          rh = exp_half(m_ref);
+        }
+        tmem_st32(s_tmem + hf * 32, pk);
+        rs += rh;
+      }
+      if (__any_sync(0xffffffffu, need)) {
+        // P_i(t-1) V has completed (it precedes S_i(t)); O_i is not read again
+        // before P_i(t) is published below
+        const uint32_t o_tmem = o_base + static_cast<uint32_t>(i * HD);
+#pragma unroll 1
+        for (int c = 0; c < HD / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(o_tmem + c * 32, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+          tmem_st32(o_tmem + c * 32, o);
+        }
+      }
+      l_sum = l_sum * alpha + rs;
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&bars->p_full[i]);
+    }
+    // ---------------- epilogue: O / l -> global -------------------------------
+    float f0, f1 = 0.f, lsev;  // factors of this thread's O and the other one's, log2-sum-exp
+    bool has1 = false;
+    if (two) {
+      f0 = live && l_sum > 0.f ? 1.f / l_sum : 0.f;
+      lsev = live && l_sum > 0.f ? m_ref + __log2f(l_sum) : -INFINITY;
+      if (live && seen && (l_sum == 0.f || !(l_sum < INFINITY) || !(fabsf(m_ref) < kMaxReference)))
+        atomicOr(&flags[ur >> 5], 1u << (ur & 31));
+      ok = ok && mbar_wait(&bars->o_done[i], 0, abort);
+    } else {
+      // merge the two halves of the key tiles: each warpgroup writes half of
+      // the columns of every row
+      ml[i * 2 * kTileM + row] = m_ref;
+      ml[i * 2 * kTileM + kTileM + row] = l_sum;
+      named_barrier_sync(1, 2 * kTileM);
+      const float m0 = ml[row], l0 = ml[kTileM + row];
+      const float m1 = ml[2 * kTileM + row], l1 = ml[3 * kTileM + row];
+      has1 = ntask[1] > 0;
+      const float mm = has1 ? fmaxf(m0, m1) : m0;
+      // a half that holds none of the row's keys has the reference -inf
+      const float a0 = m0 == -INFINITY ? 0.f : ex2_approx(m0 - mm);
+      const float a1 = has1 && m1 != -INFINITY ? ex2_approx(m1 - mm) : 0.f;
+      const float l = l0 * a0 + (has1 ? l1 * a1 : 0.f);
+      const bool far = mm != -INFINITY && !(fabsf(mm) < kMaxReference);
+      const float inv = live && l > 0.f ? 1.f / l : 0.f;
+      f0 = a0 * inv;
+      f1 = a1 * inv;
+      lsev = live && l > 0.f ? mm + __log2f(l) : -INFINITY;
+      if (live && ((seen && l == 0.f) || !(l < INFINITY) || far))
+        atomicOr(&flags[ur >> 5], 1u << (ur & 31));
+      ok = ok && mbar_wait(&bars->o_done[0], 0, abort);
+      if (has1) ok = ok && mbar_wait(&bars->o_done[1], 0, abort);
+    }
+    if (__all_sync(0xffffffffu, ok)) {
+      tc_fence_after();
+      const bool leads = two || i == 0;
+      if (leads && valid) {
+        if (partial) p.lpart[pbase + ur] = lsev;
+        else if (a.lse) a.lse[row_base + ur] = lsev * kLn2F;
+      } else if (leads && partial && ur < rows_unit) {
+        p.lpart[pbase + ur] = -INFINITY;
+      }
+      bool finite = true;
+      constexpr int kCols = HD / 32;  // 32-column pieces of a row
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) {
+        if (!two && (c / (kCols / 2)) != i) continue;
+        uint32_t o[32];
+        tmem_ld32(o_base + (two ? i * HD : 0) + c * 32, o);
+        tmem_wait_ld();
+        if (!two) {
+          uint32_t o1[32];
+          if (has1) {
+            tmem_ld32(o_base + HD + c * 32, o1);
+            tmem_wait_ld();
+          }
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            o[k] = __float_as_uint((f0 > 0.f ? __uint_as_float(o[k]) * f0 : 0.f) +
+                                   (f1 > 0.f ? __uint_as_float(o1[k]) * f1 : 0.f));
+        }
+        const float f = two ? f0 : 1.f;
+        float sum = 0.f;  // NaN when a value is not finite
+#pragma unroll
+        for (int k = 0; k < 32; ++k) sum += __uint_as_float(o[k]) * 0.f;
+        finite = finite && sum == 0.f;
+        if (!live) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = 0u;
+        }
+        if (valid) {
+          if (partial) store_row32(p.opart + (pbase + ur) * HD + c * 32, o, f);
+          else store_row32(out + (row_base + ur) * HD + c * 32, o, f);
+        }
+      }
+      if (live && !finite) atomicOr(&flags[ur >> 5], 1u << (ur & 31));
+    }
+  }
+  __syncthreads();
+  const bool aborted = *abort != 0;
+  if (aborted && threadIdx.x == 0) raise_status(a.stats, SPARSEPR_ERR_TIMEOUT);
+  if (warp == 0) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+  if (aborted) return;
+  // Rows whose result is not finite: a hidden key with NaN or infinity in the same
+  // tile, or a visible one. They are taken again by the definition.
+  LiteralScratch<kThreads>& scratch = *reinterpret_cast<LiteralScratch<kThreads>*>(smem);
+  float* q = reinterpret_cast<float*>(smem + 8192);
+  for (int w = 0; w < 8; ++w) {
+    uint32_t todo = flags[w];
+    while (todo) {
+      const int ur = w * 32 + __ffs(todo) - 1;
+      todo &= todo - 1;
+      const size_t row = row_base + ur;
+      const __nv_bfloat16* kbase = static_cast<const __nv_bfloat16*>(a.k);
+      const __nv_bfloat16* vbase = static_cast<const __nv_bfloat16*>(a.v);
+      const size_t kvoff = static_cast<size_t>(kvh) * a.Nk * HD;
+      const TileKV<HD> kv = {kbase + kvoff, vbase + kvoff, u};
+      for (int c = threadIdx.x; c < HD; c += kThreads)
+        q[c] = load_f32(static_cast<const __nv_bfloat16*>(a.q) + row * HD + c);
+      __syncthreads();
+      float m, l, o;
+      literal_row<kThreads, HD>(kv, q, visible_range(a.see, pos0 + (r0 + ur) % a.Nq, len), a.sc,
+                                scratch, m, l, o);
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const float lsev = l == 0.f ? -INFINITY : m + log2f(l);
+      if (threadIdx.x < HD) {
+        if (partial) p.opart[(pbase + ur) * HD + threadIdx.x] = o * inv;
+        else store_f32(out + row * HD + threadIdx.x, o * inv);
+      }
+      if (threadIdx.x == 0) {
+        if (partial) p.lpart[pbase + ur] = lsev;
+        else if (a.lse) a.lse[row] = lsev * kLn2F;
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// out = sum_s 2^(l_s - M) O_s / sum_s 2^(l_s - M), M = max_s l_s, over the splits'
+// normalised partial outputs in a fixed order; a split without any of the
+// row's keys has l_s = -inf and is not read. Thread = (row, 4 columns).
+template <typename T>
+__global__ void __launch_bounds__(256) window_combine_kernel(const WindowKernelParams p) {
+  const WindowArgs& a = p.a;
+  const int d = a.d, cpr = d / 4;
+  const int unit = blockIdx.y, seg = unit / p.tiles, tile = unit % p.tiles;
+  const int r = blockIdx.x * (256 / cpr) + threadIdx.x / cpr, c = (threadIdx.x % cpr) * 4;
+  const int r0 = tile * p.unit_rows;
+  const int bh0 = p.R != a.Nq ? seg * p.group : seg;
+  const int n = clamp_count(a.n_q, bh0 / a.Hq, a.Nq, a.Nq, a.stats, false);
+  if (r0 + r >= p.R || r >= p.unit_rows || (r0 + r) % a.Nq >= n) return;
+  const size_t base = static_cast<size_t>(unit) * p.splits * p.unit_rows + r;
+  float M = -INFINITY;
+  bool nan = false;
+  for (int s = 0; s < p.splits; ++s) {
+    const float l = p.lpart[base + static_cast<size_t>(s) * p.unit_rows];
+    M = fmaxf(M, l);
+    nan = nan || l != l;
+  }
+  float num[4] = {0.f, 0.f, 0.f, 0.f}, den = 0.f;
+  for (int s = 0; s < p.splits; ++s) {
+    const size_t at = base + static_cast<size_t>(s) * p.unit_rows;
+    const float l = p.lpart[at];
+    if (l == -INFINITY) continue;
+    const float w = exp2f(l - M);
+    const float4 o = *reinterpret_cast<const float4*>(p.opart + at * d + c);
+    num[0] = fmaf(w, o.x, num[0]);
+    num[1] = fmaf(w, o.y, num[1]);
+    num[2] = fmaf(w, o.z, num[2]);
+    num[3] = fmaf(w, o.w, num[3]);
+    den += w;
+  }
+  const float inv = den > 0.f || nan ? 1.f / den : 0.f;
+  const size_t row = static_cast<size_t>(bh0) * a.Nq + r0 + r;
+  T* o = static_cast<T*>(a.out) + row * d + c;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) store_f32(o + e, num[e] * inv);
+  if (a.lse && c == 0)
+    a.lse[row] = nan ? num[0] * 0.f + den : den > 0.f ? (M + log2f(den)) * kLn2F : -INFINITY;
+}
+
+bool make_map2(CUtensorMap* m, const void* base, size_t rows, int d, int box_rows) {
+  EncodeTiledFn enc = encode_tiled_fn();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(d) * 2};
+  cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t es[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
+             es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// [heads, rows, d]: rows past a head's end read as zero
+bool make_map3(CUtensorMap* m, const void* base, int heads, int rows, int d, int box_rows) {
+  EncodeTiledFn enc = encode_tiled_fn();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(rows),
+                        static_cast<cuuint64_t>(heads)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2,
+                           static_cast<cuuint64_t>(rows) * d * 2};
+  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+             es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int HD, typename T>
+cudaError_t launch_hd(const WindowKernelParams& p, const WindowMaps& maps, int units,
+                      cudaStream_t st) {
+  cudaError_t e = cudaFuncSetAttribute(window_attn_kernel<HD, T>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       kSmemBytes);
+  if (e != cudaSuccess) return e;
+  window_attn_kernel<HD, T><<<static_cast<unsigned>(units) * p.splits, kThreads, kSmemBytes,
+                              st>>>(maps, p);
+  if (p.splits > 1) {
+    const int rows = 256 / (HD / 4);
+    const dim3 grid((p.unit_rows + rows - 1) / rows, units);
+    window_combine_kernel<T><<<grid, 256, 0, st>>>(p);
+  }
+  return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_window_attention(const WindowArgs& a, cudaStream_t st) {
-  if (a.Nq == 0) return cudaSuccess;
-  const dim3 grid(a.Nq, a.B * a.Hq);
-  if (a.bf16) {
-    if (a.d == 128) window_rows_kernel<__nv_bfloat16, 128><<<grid, kRowThreads, 0, st>>>(a);
-    else window_rows_kernel<__nv_bfloat16, 64><<<grid, kRowThreads, 0, st>>>(a);
-  } else {
-    if (a.d == 128) window_rows_kernel<float, 128><<<grid, kRowThreads, 0, st>>>(a);
-    else window_rows_kernel<float, 64><<<grid, kRowThreads, 0, st>>>(a);
+// How the rows are cut, from the sizes alone.
+//   - Short query runs of heads that share a key head are packed into one tile:
+//     their rows are contiguous, and the tile's 128 rows are filled.
+//   - Units of 256 rows (two tiles, each key tile read once for both) unless
+//     that leaves multiprocessors without a unit; then units of 128 rows.
+//   - With fewer units than multiprocessors the key tiles of a unit are split
+//     over several blocks, at least two tiles each, and joined afterwards.
+WindowPlan window_plan(int B, int Hq, int Hkv, int Nq, int Nk, const sparsepr_visibility& see) {
+  WindowPlan w = {};
+  const int group = Hq / Hkv;
+  const bool pack = group > 1 && Nq < kTileM;
+  w.R = pack ? group * Nq : Nq;
+  w.segs = pack ? B * Hkv : B * Hq;
+  w.unit_rows = 2 * kTileM;
+  w.tiles = (w.R + w.unit_rows - 1) / w.unit_rows;
+  if (w.R <= kTileM || static_cast<long long>(w.segs) * w.tiles < kPlanSMs) {
+    w.unit_rows = kTileM;
+    w.tiles = (w.R + w.unit_rows - 1) / w.unit_rows;
   }
-  return cudaGetLastError();
+  const long long units = static_cast<long long>(w.segs) * w.tiles;
+  w.splits = 1;
+  if (units < kPlanSMs) {
+    long long keys = Nk;
+    if (see.window > 0) {
+      const long long F = see.frame;
+      const long long span = (see.sinks + (see.causal ? 1ll : 2ll) * see.window + 1) * F + w.unit_rows;
+      if (span < keys) keys = span;
+    }
+    const long long key_tiles = (keys + kTileN - 1) / kTileN;
+    long long s = kPlanSMs / units;
+    if (s > kMaxWindowSplits) s = kMaxWindowSplits;
+    if (s > key_tiles / 2) s = key_tiles / 2;
+    if (s > 1) w.splits = static_cast<int>(s);
+  }
+  w.units = static_cast<int>(units);
+  return w;
+}
+
+cudaError_t launch_window_attention(const WindowArgs& in, cudaStream_t st) {
+  WindowKernelParams p = {};
+  p.a = in;
+  WindowArgs& a = p.a;
+  if (a.Nq == 0) return cudaSuccess;
+  const WindowPlan w = window_plan(a.B, a.Hq, a.Hkv, a.Nq, a.Nk, a.see);
+  p.group = a.Hq / a.Hkv;
+  p.R = w.R;
+  p.segs = w.segs;
+  p.tiles = w.tiles;
+  p.unit_rows = w.unit_rows;
+  p.splits = w.splits;
+  p.opart = a.opart;
+  p.lpart = a.lpart;
+  const size_t q_rows = static_cast<size_t>(a.B) * a.Hq * a.Nq;
+  const size_t kv_rows = static_cast<size_t>(a.B) * a.Hkv * a.Nk;
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const bool f32 = !a.bf16;
+  if (f32) {  // the MMAs take bf16
+    if ((e = launch_cast_bf16(static_cast<const float*>(a.q), a.qb, q_rows * a.d, st)) != cudaSuccess)
+      return e;
+    a.q = a.qb;
+    if (kv_rows > 0) {
+      if ((e = launch_cast_bf16(static_cast<const float*>(a.k), a.kb, kv_rows * a.d, st)) != cudaSuccess ||
+          (e = launch_cast_bf16(static_cast<const float*>(a.v), a.vb, kv_rows * a.d, st)) != cudaSuccess)
+        return e;
+      a.k = a.kb;
+      a.v = a.vb;
+    }
+  }
+  WindowMaps maps;
+  p.q_box_rows = q_rows < static_cast<size_t>(kTileM) ? static_cast<int>(q_rows) : kTileM;
+  // without keys no tile is read; the maps then describe the queries
+  p.kv_box_rows = a.Nk < kTileN ? max(a.Nk, 1) : kTileN;
+  if (!make_map2(&maps.q, a.q, q_rows, a.d, p.q_box_rows)) return cudaErrorInvalidValue;
+  if (a.Nk > 0) {
+    if (!make_map3(&maps.k, a.k, a.B * a.Hkv, a.Nk, a.d, p.kv_box_rows) ||
+        !make_map3(&maps.v, a.v, a.B * a.Hkv, a.Nk, a.d, p.kv_box_rows))
+      return cudaErrorInvalidValue;
+  } else {
+    maps.k = maps.q;
+    maps.v = maps.q;
+  }
+  if (a.d == 128)
+    return f32 ? launch_hd<128, float>(p, maps, w.units, st)
+               : launch_hd<128, __nv_bfloat16>(p, maps, w.units, st);
+  return f32 ? launch_hd<64, float>(p, maps, w.units, st)
+             : launch_hd<64, __nv_bfloat16>(p, maps, w.units, st);
 }
 
 }  // namespace spr

@@ -133,9 +133,14 @@ size_t carve_cache(const sparsepr_cache_params& p, char* base, CacheArgs* a) {
 size_t carve_cache_attention(const sparsepr_cache_params& p,
                              const sparsepr_cache_attention_params& q, char* base,
                              CacheAttnArgs* a) {
-  (void)q;
   Carver w{base};
   w.at = carve_cache(p, base, &a->cache);
+  if (q.Nq > 0) {
+    const CacheAttnPlan plan = cache_attn_plan(p, q.Hq, q.Nq);
+    a->pre = w.take<int32_t>(p.B + 1);
+    a->opart = w.take<float>(plan.slots * plan.slot_rows * p.d);
+    a->lpart = w.take<float>(plan.slots * plan.slot_rows);
+  }
   return w.at;
 }
 

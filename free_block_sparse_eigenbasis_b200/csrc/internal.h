@@ -363,7 +363,16 @@ struct CacheAttnArgs {
   sparsepr_visibility see;
   float sc;  // scale * log2(e)
   bool bf16;
+  // scratch in the workspace
+  int32_t* pre;          // [B + 1] tiles before each sequence
+  float *opart, *lpart;  // partial outputs and log2-sum-exps of units cut over blocks
 };
+struct CacheAttnPlan {
+  int row_tiles;   // tiles of query rows per key head
+  size_t slots;    // partial results
+  int slot_rows;   // rows of each
+};
+CacheAttnPlan cache_attn_plan(const sparsepr_cache_params& p, int Hq, int Nq);
 cudaError_t launch_cache_attention(const CacheAttnArgs& a, cudaStream_t st);
 
 cudaError_t launch_pairs_exec(const int64_t* pairs_sparse, int H, int64_t add, int64_t* pairs_exec,

@@ -65,16 +65,23 @@ __device__ __forceinline__ void store_f32(float* p, float v) { *p = v; }
 // Returns the maximum m (log2 units, sc = scale * log2 e), the sum l and, in
 // thread c < D, the unnormalised output o of column c; l is NaN for a row whose
 // visible logits are all -inf, and 0 for a row that sees nothing.
+// Called by the NT threads 0..NT-1 of a block, which `sync` joins.
 template <int NT>
 struct LiteralScratch {
   float p[NT];
   float o[NT];
   float red[32];
+  int any[32];
 };
 
-template <int NT, int D, class KV>
+struct BlockSync {
+  __device__ void operator()() const { __syncthreads(); }
+};
+
+template <int NT, int D, class KV, class Sync>
 __device__ void literal_row(const KV& kv, const float* q, const Range r, float sc,
-                            LiteralScratch<NT>& sm, float& m_out, float& l_out, float& o_out) {
+                            LiteralScratch<NT>& sm, const Sync& sync, float& m_out, float& l_out,
+                            float& o_out) {
   constexpr int kGroups = NT / D;
   static_assert(kGroups >= 1 && NT % 32 == 0, "threads");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -94,16 +101,23 @@ __device__ void literal_row(const KV& kv, const float* q, const Range r, float s
     float mx = on ? x : -INFINITY;
 #pragma unroll
     for (int w = 16; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-    if (lane == 0) sm.red[warp] = mx;
-    seen = __syncthreads_or(on) || seen;
-    for (int w = 0; w < NT / 32; ++w) mx = fmaxf(mx, sm.red[w]);
+    const bool any = __any_sync(0xffffffffu, on);
+    if (lane == 0) {
+      sm.red[warp] = mx;
+      sm.any[warp] = any;
+    }
+    sync();
+    for (int w = 0; w < NT / 32; ++w) {
+      mx = fmaxf(mx, sm.red[w]);
+      seen = seen || sm.any[w];
+    }
     const float mn = fmaxf(m, mx);
     const float corr = (m == -INFINITY) ? 0.f : exp2f(m - mn);
     // weight of this thread's key; -1 marks a key that is not there
     float p = -1.f;
     if (on) p = (mn == -INFINITY) ? (x == x ? 0.f : x) : exp2f(x - mn);
     sm.p[tid] = p;
-    __syncthreads();
+    sync();
     float sum = 0.f;
     const int n = min(NT, total - base);
     for (int i = 0; i < n; ++i) {  // the same order in every thread
@@ -120,14 +134,14 @@ __device__ void literal_row(const KV& kv, const float* q, const Range r, float s
         o += w * kv.v(u < r.s ? u : r.lo + (u - r.s), c);
       }
     m = mn;
-    __syncthreads();
+    sync();
   }
   sm.o[tid] = o;
-  __syncthreads();
+  sync();
   if (tid < D)
     for (int g = 1; g < kGroups; ++g) o += sm.o[g * D + tid];
   if (seen && l == 0.f) l = __int_as_float(0x7fc00000);
-  __syncthreads();
+  sync();
   m_out = m;
   l_out = l;
   o_out = o;

@@ -660,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncthreads();
       float m, l, o;
       literal_row<kThreads, HD>(kv, q, visible_range(a.see, pos0 + (r0 + ur) % a.Nq, len), a.sc,
-                                scratch, m, l, o);
+                                scratch, BlockSync{}, m, l, o);
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const float lsev = l == 0.f ? -INFINITY : m + log2f(l);
       if (threadIdx.x < HD) {

@@ -138,8 +138,8 @@ size_t carve_cache_attention(const sparsepr_cache_params& p,
   if (q.Nq > 0) {
     const CacheAttnPlan plan = cache_attn_plan(p, q.Hq, q.Nq);
     a->pre = w.take<int32_t>(p.B + 1);
-    a->opart = w.take<float>(plan.slots * plan.slot_rows * p.d);
-    a->lpart = w.take<float>(plan.slots * plan.slot_rows);
+    a->opart = w.take<float>(plan.slots * plan.rows * p.d);
+    a->lpart = w.take<float>(plan.slots * plan.rows);
   }
   return w.at;
 }

@@ -22,65 +22,76 @@
 namespace spr {
 namespace {
 
-constexpr int kTile = 64;            // keys of a tile, at multiples of 64 in the sequence
-constexpr int kWarps = 8;            // consumer warps, each takes every 8th tile of the block
-constexpr int kConsumers = kWarps * 32;
-constexpr int kDecodeThreads = kConsumers + 32;  // and a producer warp
-constexpr int kRows = 16;            // query rows of a block: the M of the MMA
-constexpr int kDecodeBlocks = 148;   // one per multiprocessor
-constexpr int kMinTiles = 4;         // tiles per block at least (they go to different warps)
+constexpr int kWarps = 6;            // 168 registers a thread
+constexpr int kDecodeThreads = kWarps * 32;
+constexpr int kMaxRows = 16;         // query rows of a block at most: 8 for each NT
+constexpr int kDecodeBlocks = 296;   // two per multiprocessor: one streams while the other merges
+constexpr int kMinTiles = kWarps;    // tiles per block at least (each goes to another warp)
+constexpr int kDepth = 2;            // tiles of a warp: one in hand, one on its way
 
-template <int HD>
+// keys of a tile, at multiples of that in the sequence: 4 KB of keys and of values
+__host__ __device__ constexpr int tile_keys(int d) { return 4096 / d; }
+
+template <int HD, int NT>
 struct DecodeSmem {
-  static constexpr int kTileBytes = kTile * HD;            // keys or values of a tile
+  static constexpr int kTileBytes = 4096;
   static constexpr int kStageBytes = 2 * kTileBytes;
-  static constexpr int kStages = HD == 128 ? 8 : 16;       // 128 KB in flight
-  static constexpr int stage_off = 0;
-  static constexpr int merge_off = kStages * kStageBytes;  // [8 warps][HD / 2][32] fp32
-  static constexpr int merge_bytes = kWarps * (HD / 2) * 32 * 4;
+  static constexpr int kStages = kWarps * kDepth;          // 96 KB
+  static constexpr int kRegs = HD / 16 * NT * 4;           // accumulators of a lane
+  static constexpr int merge_off = kStages * kStageBytes;  // [kMergeWarps][kRegs][32] fp32
+  static constexpr int merge_bytes = 8192;
+  static constexpr int kMergeWarps = merge_bytes / (kRegs * 128) < kWarps
+                                         ? merge_bytes / (kRegs * 128) : kWarps;
   static constexpr int pre_off = merge_off + merge_bytes;  // [1025] tiles before each sequence
-  static constexpr int misc_off = pre_off + 1032 * 8;
-  static constexpr int misc_bytes = 8192;
+  static constexpr int misc_off = pre_off + 1028 * 4;
+  static constexpr int misc_bytes = 3072;
   static constexpr int bytes = misc_off + misc_bytes + 1024;
+  // two blocks per multiprocessor (228 KB, 1 KB of it reserved for each block)
+  static_assert(2 * (bytes + 1024) <= 228 * 1024, "shared memory");
 };
 
 struct DecodeMisc {
-  uint64_t full[16], empty[16];
-  float k_scale[16][4], v_log2[16][4];  // per stage and page of the tile; k_scale < 0: no page
-  float m[kWarps][kRows], M[kWarps][kRows], l[kWarps][kRows];
-  int seen[kWarps][kRows];
-  long long warp_sums[16];
+  uint64_t full[kWarps][kDepth];
+  float m[kWarps][kMaxRows], M[kWarps][kMaxRows], l[kWarps][kMaxRows];
+  int seen[kWarps][kMaxRows];
+  Range range[kMaxRows];                // of the run's query rows
+  float q_scale[kMaxRows];
+  int live[kMaxRows], valid[kMaxRows];  // the row sees a key; the row is in use
+  int warp_sums[kWarps];
   uint32_t flags;
   int abort;
   float q[128];
 };
-static_assert(sizeof(DecodeMisc) + sizeof(LiteralScratch<kConsumers>) + 64 <= 8192, "misc");
+static_assert(sizeof(DecodeMisc) <= 3072, "misc");
+static_assert(sizeof(LiteralScratch<kDecodeThreads>) <= 8192, "it shares the merge buffer");
 
 struct DecodeMaps {
-  CUtensorMap k, v;  // [n_pages, Hkv * page, HD] bytes, boxes of min(page, 64) rows
+  CUtensorMap k, v;  // [n_pages, Hkv * page, HD] bytes, boxes of min(page, tile) rows
 };
 
 struct DecodeParams {
   CacheAttnArgs a;
   int group;       // query heads per key head
   int R;           // query rows per key head: group * Nq, contiguous in q
-  int row_tiles;   // ceil(R / 16)
+  int rows;        // query rows of a unit: 8 or 16
+  int row_tiles;   // ceil(R / rows)
   int units_seq;   // Hkv * row_tiles
-  int sub_rows;    // min(page, 64): rows of one copy
+  int sub_rows;    // min(page, tile): rows of one copy
   int* pre;        // [B + 1] in the workspace: tiles before each sequence (for the combine)
-  float* opart;    // [B * units_seq + blocks, 16, HD]
-  float* lpart;    // [B * units_seq + blocks, 16]
+  float* opart;    // [B * units_seq + blocks, rows, HD]
+  float* lpart;    // [B * units_seq + blocks, rows]
 };
 
 // Tiles that the queries of a sequence need: 0..TA-1, then from TB on.
 struct SeqTiles {
   int L, n;        // keys, queries
   int SA, LB, HB;  // keys that some query sees: [0, SA) and [LB, HB)
+  int tile;        // keys of a tile
   int TA, TB, T;
-  __device__ int start(int t) const { return (t < TA ? t : TB + (t - TA)) * kTile; }
+  __device__ int start(int t) const { return (t < TA ? t : TB + (t - TA)) * tile; }
   // index of the tile that holds a visible key
   __device__ int tile_of(int j) const {
-    const int x = j / kTile;
+    const int x = j / tile;
     return x < TA ? x : TA + (x - TB);
   }
 };
@@ -99,9 +110,11 @@ __device__ __forceinline__ SeqTiles seq_tiles(const CacheAttnArgs& a, int b, boo
     s.LB = first.lo;
     s.HB = max(last.hi, s.LB);
   }
-  s.TA = (s.SA + kTile - 1) / kTile;
-  s.TB = max(s.LB / kTile, s.TA);
-  s.T = s.TA + max((s.HB + kTile - 1) / kTile - s.TB, 0);
+  const int tile = tile_keys(c.p.d);
+  s.tile = tile;
+  s.TA = (s.SA + tile - 1) / tile;
+  s.TB = max(s.LB / tile, s.TA);
+  s.T = s.TA + max((s.HB + tile - 1) / tile - s.TB, 0);
   return s;
 }
 
@@ -149,11 +162,17 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
 // D (16x8, fp32) += A (16x16, fp16) B (16x8, fp16)
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// transpose of an 8x8 matrix of 16-bit values (lane 4 r + c holds row r, columns 2c, 2c + 1)
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
 }
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
@@ -179,32 +198,35 @@ __device__ __forceinline__ int blocks_for(long long total) {
   return static_cast<int>(want < kDecodeBlocks ? (want > 0 ? want : 1) : kDecodeBlocks);
 }
 
-struct ConsumerSync {
-  __device__ void operator()() const { named_barrier_sync(1, kConsumers); }
-};
-
-// Few query rows. The tiles of all (sequence, key head, 16 query rows) units form
-// one line that is cut evenly over the blocks, whatever the lengths: a block
-// takes a run of it, which may end one unit, hold several and begin another.
-// A producer warp looks pages up and streams keys and values by TMA, 128 KB in
-// flight; consumer warp w takes every 8th tile and keeps its own running
-// maxima, sum and 16 x HD accumulator (in registers, flat over the tile's
-// pages); at the end of a unit's run the eight are merged, and runs that do not
-// hold the whole unit leave a partial result for cache_combine_kernel.
+// Few query rows. The tiles of all (sequence, key head, 8 or 16 query rows)
+// units form one line that is cut evenly over the blocks, whatever the lengths:
+// a block takes a run of it, which may end one unit, hold several and begin
+// another. Of a run, warp w takes every 12th tile: it looks the pages up (32 at a
+// time, ahead), fetches keys and values by TMA into its own two stages and keeps
+// its own running maxima, sum and accumulator in registers, so that warps do not
+// wait for one another (one warp that fetched for all was the bound: 3.3 TB/s).
+// The first tiles of the next run are fetched before the warps are merged at
+// the end of a run; a run that does not hold its whole unit leaves a partial
+// result for cache_combine_kernel.
 //
-// Fragments of mma m16n8k16 (g = lane / 4, t = lane % 4). The order of d
-// within a product and the order of the output columns are free, so a lane takes
-// 16 contiguous bytes: of key g (8 keys per product), d = 16 c .. 16 c + 15 at
-// chunk c = 2 t + u (HD = 128; c = t for 64), 4 bytes for each step of 16; and of the four
-// values 2t, 2t+1, 2t+8, 2t+9 the columns (HD / 8) g .. The tile is swizzled by
-// TMA, so that the lanes of a quarter warp meet different banks.
-template <int HD, typename T>
-__global__ void __launch_bounds__(kDecodeThreads, 1)
+// Both products have the cache as the 16-row operand (keys, then columns of V) and
+// the query rows as the 8 columns: x^T = K q^T, o^T = V^T p^T. Fragments of mma
+// m16n8k16 (g = lane / 4, t = lane % 4). The order of d within a product and
+// the order of the output columns are free, so a lane takes 16 contiguous bytes:
+// of keys g and g + 8, d = 16 c .. 16 c + 15 at chunk c = 2 t + u (HD = 128; c = t for
+// 64), 4 bytes for each step of 16; and of the values 2t, 2t+1, 2t+8, 2t+9 the
+// columns (HD / 8) g .. The tile is swizzled by TMA, so that the lanes of a
+// quarter warp meet different banks. The weights are turned into the second
+// product's operand by an 8x8 transpose.
+template <int HD, int NT, typename T>
+__global__ void __launch_bounds__(kDecodeThreads, 2)
     cache_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeParams p) {
-  using L = DecodeSmem<HD>;
+  using L = DecodeSmem<HD, NT>;
+  constexpr int kTile = tile_keys(HD);
+  constexpr int kRows = 8 * NT;
   constexpr int kU = HD / 64;        // 16-byte pieces of a key per lane
-  constexpr int kSteps = HD / 16;    // steps of the first product
-  constexpr int kNd = HD / 8;        // column tiles of the second product
+  constexpr int kSteps = HD / 16;    // steps of the first product, row tiles of the second
+  constexpr int kKt = kTile / 16;    // row tiles of the first product, steps of the second
   const CacheAttnArgs& a = p.a;
   const CacheArgs& c = a.cache;
   const int B = c.p.B, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -213,51 +235,50 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   float* merge = reinterpret_cast<float*>(smem + L::merge_off);
-  long long* pre = reinterpret_cast<long long*>(smem + L::pre_off);
+  int* pre = reinterpret_cast<int*>(smem + L::pre_off);
   DecodeMisc& ms = *reinterpret_cast<DecodeMisc*>(smem + L::misc_off);
-  LiteralScratch<kConsumers>& scratch = *reinterpret_cast<LiteralScratch<kConsumers>*>(
-      smem + L::misc_off + (sizeof(DecodeMisc) + 63) / 64 * 64);
+  LiteralScratch<kDecodeThreads>& scratch =
+      *reinterpret_cast<LiteralScratch<kDecodeThreads>*>(smem + L::merge_off);
 
-  // tiles before each sequence: a thread counts four sequences, the block scans
-  {
-    long long mine[4], sum = 0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int b = tid * 4 + e;
-      mine[e] = b < B ? seq_tiles(a, b, blockIdx.x == 0).T : 0;
-      sum += mine[e];
-    }
-    long long x = sum;
+  // the combine kernel may be put in place as blocks end; it waits for all of them
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (tid == 0) {
+    for (int s = 0; s < L::kStages; ++s) mbar_init(&ms.full[0][0] + s, 1);
+    ms.abort = 0;
+    ms.flags = 0;
+    fence_barrier_init();
+  }
+  // tiles before each sequence
+  int carry = 0;
+  for (int b0 = 0; b0 < B; b0 += kDecodeThreads) {
+    const int b = b0 + tid;
+    const int mine = b < B ? seq_tiles(a, b, blockIdx.x == 0).T : 0;
+    int x = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
       if (lane >= o) x += y;
     }
     if (lane == 31) ms.warp_sums[warp] = x;
-    if (tid == 0) {
-      for (int s = 0; s < L::kStages; ++s) {
-        mbar_init(&ms.full[s], 1);
-        mbar_init(&ms.empty[s], 1);
-      }
-      ms.abort = 0;
-      ms.flags = 0;
-      fence_barrier_init();
-    }
     __syncthreads();
-    long long before = x - sum;
-    for (int w = 0; w < warp; ++w) before += ms.warp_sums[w];
+    int before = carry + x - mine;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int b = tid * 4 + e;
-      if (b <= B) {
-        pre[b] = before;
-        if (blockIdx.x == 0) p.pre[b] = static_cast<int>(before);
-      }
-      before += mine[e];
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += ms.warp_sums[w];
+      carry += ms.warp_sums[w];
+    }
+    if (b < B) {
+      pre[b] = before;
+      if (blockIdx.x == 0) p.pre[b] = before;
     }
     __syncthreads();
   }
-  const long long total = pre[B] * p.units_seq;
+  if (tid == 0) {
+    pre[B] = carry;
+    if (blockIdx.x == 0) p.pre[B] = carry;
+  }
+  __syncthreads();
+  const long long total = static_cast<long long>(carry) * p.units_seq;
   const int blocks = blocks_for(total);
   if (total == 0 || static_cast<int>(blockIdx.x) >= blocks) return;
   const long long begin = total * blockIdx.x / blocks, end = total * (blockIdx.x + 1) / blocks;
@@ -271,264 +292,339 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     int lo = 0, hi = B;  // pre[lo] * units <= pos < pre[hi] * units
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
-      if (pre[mid] * p.units_seq <= pos) lo = mid;
+      if (static_cast<long long>(pre[mid]) * p.units_seq <= pos) lo = mid;
       else hi = mid;
     }
-    const long long tiles = pre[lo + 1] - pre[lo], off = pos - pre[lo] * p.units_seq;
+    const int tiles = pre[lo + 1] - pre[lo];
+    const long long off = pos - static_cast<long long>(pre[lo]) * p.units_seq;
     Run r;
     r.b = lo;
-    r.x = static_cast<int>(off / tiles);
-    r.t0 = static_cast<int>(off % tiles);
-    r.t1 = static_cast<int>(min(tiles, r.t0 + (end - pos)));
+    r.x = (off >> 31) == 0 ? static_cast<int>(static_cast<uint32_t>(off) / static_cast<uint32_t>(tiles))
+                           : static_cast<int>(off / tiles);
+    r.t0 = static_cast<int>(off - static_cast<long long>(r.x) * tiles);
+    r.t1 = static_cast<int>(min(static_cast<long long>(tiles), r.t0 + (end - pos)));
     return r;
   };
+  const int sub = p.sub_rows, spp = kTile / sub;  // rows of a copy, copies of a tile: 1, 2, 4
+  const int sub_shift = 31 - __clz(sub), page_shift = 31 - __clz(c.p.page);
+  const int part = lane & (spp - 1), per_batch = 32 / spp;
 
-  if (warp == kWarps) {
-    // ------------------------------ producer ---------------------------------
-    const int sub = p.sub_rows, spp = kTile / sub;  // copies of a tile (for keys, for values)
-    const int page = c.p.page;
-    int issued = 0;  // tiles of this block so far
-    bool ok = true;
-    for (long long pos = begin; pos < end && ok;) {
-      const Run r = run_at(pos);
-      const SeqTiles s = seq_tiles(a, r.b, false);
-      const int h = r.x / p.row_tiles;
-      const int32_t* row = c.c.table + static_cast<size_t>(r.b) * c.p.max_pages;
-      // 32 pages (or halves of one) are looked up at a time
-      const int per_batch = 32 / spp;
-      for (int t = r.t0; t < r.t1 && ok; t += per_batch) {
-        const int mine = t + lane / spp;  // this lane's tile
-        int id = -1, key0 = 0;
-        float ks = -1.f, lv = 0.f;
-        if (mine < r.t1) {
-          key0 = s.start(mine) + (lane % spp) * sub;
-          // keys of this copy that some query sees
-          const bool wanted = key0 < s.SA || (key0 < s.HB && key0 + sub > s.LB);
-          if (wanted) {
-            id = row[key0 / page];
-            if (id < 0 || id >= c.p.n_pages) {
-              raise_status(c.stats, SPARSEPR_ERR_INVALID_ARG);
-              id = -1;
-            } else {
-              const size_t slot = static_cast<size_t>(id) * c.p.Hkv + h;
-              ks = fabsf(c.c.k_scale[slot]);
-              lv = log2_of_scale(c.c.v_scale[slot]);
-            }
-          }
-        }
-        const unsigned have = __ballot_sync(0xffffffffu, id >= 0);
-        const int here = min(per_batch, r.t1 - t);
-        for (int e = 0; e < here && ok; ++e, ++issued) {
-          const int st = issued % L::kStages, round = issued / L::kStages;
-          if (lane == 0 && round > 0) ok = mbar_wait(&ms.empty[st], (round + 1) & 1, abort);
-          ok = __shfl_sync(0xffffffffu, ok, 0);
-          if (!ok) break;
-          const bool part = lane / spp == e;  // lanes of this tile
-          if (part) {
-            ms.k_scale[st][lane % spp] = ks;
-            ms.v_log2[st][lane % spp] = lv;
-          }
-          __syncwarp();
-          const unsigned tile_lanes = ((spp == 32 ? 0u : (1u << spp)) - 1u) << (e * spp);
-          if (lane == 0)
-            mbar_arrive_expect_tx(&ms.full[st], __popc(have & tile_lanes) * 2 * sub * HD);
-          __syncwarp();
-          if (part && id >= 0) {
-            uint8_t* dst = smem + L::stage_off + st * L::kStageBytes + (lane % spp) * sub * HD;
-            const int y = h * page + key0 % page;
-            tma_load_3d(dst, &maps.k, &ms.full[st], 0, y, id);
-            tma_load_3d(dst + L::kTileBytes, &maps.v, &ms.full[st], 0, y, id);
-          }
+  // ---- fetching: tile k of the warp is tile warp + 12 k of its run ----
+  struct Look {  // one copy: page (-1: none to fetch), first key, scales
+    int id, key0;
+    float ks, vs;
+  };
+  struct Fetch {
+    Run r;
+    SeqTiles s;
+    int h, count, batch;  // key head, tiles of this warp, first tile of `now`
+    Look now, next;
+    float ks0, vs0;       // scales of the batch before `now`, whose last tiles are still in use
+  } f = {};
+  uint32_t fetched = 0;  // tiles of this warp so far
+  uint8_t* const my_stages = smem + warp * kDepth * L::kStageBytes;
+  auto look_up = [&](int k0) {
+    Look x = {-1, 0, -1.f, 1.f};
+    const int k = k0 + lane / spp;  // this lane's tile
+    if (k < f.count) {
+      x.key0 = f.s.start(f.r.t0 + warp + k * kWarps) + part * sub;
+      // keys of this copy that some query sees
+      if (x.key0 < f.s.SA || (x.key0 < f.s.HB && x.key0 + sub > f.s.LB)) {
+        x.id = c.c.table[static_cast<size_t>(f.r.b) * c.p.max_pages + (x.key0 >> page_shift)];
+        if (x.id < 0 || x.id >= c.p.n_pages) {
+          raise_status(c.stats, SPARSEPR_ERR_INVALID_ARG);
+          x.id = -1;
         }
       }
-      pos += r.t1 - r.t0;
     }
-    // let the copies in flight land before the block goes on
-    if (lane == 0) {
-      volatile int never = 0;
-      for (int n = max(0, issued - L::kStages); n < issued; ++n)
-        mbar_wait(&ms.full[n % L::kStages], (n / L::kStages) & 1, &never);
+    return x;
+  };
+  // first needed when a tile is in hand: these loads pass behind its copy
+  auto look_up_scales = [&](Look& x) {
+    if (x.id >= 0) {
+      const size_t slot = static_cast<size_t>(x.id) * c.p.Hkv + f.h;
+      x.ks = fabsf(c.c.k_scale[slot]);
+      x.vs = c.c.v_scale[slot];
     }
-  } else {
-    // ------------------------------ consumers --------------------------------
+  };
+  auto fetch = [&](int k) {
+    if (__any_sync(0xffffffffu, *abort != 0)) return;
+    if (k == f.batch + per_batch) {
+      f.ks0 = f.now.ks;
+      f.vs0 = f.now.vs;
+      f.now = f.next;
+      f.batch = k;
+      f.next = look_up(k + per_batch);
+      look_up_scales(f.next);
+    }
+    const int st = fetched % kDepth;
+    const bool load = lane / spp == k - f.batch && f.now.id >= 0;  // lanes of this tile
+    const unsigned have = __ballot_sync(0xffffffffu, load);
+    uint64_t* bar = &ms.full[warp][st];
+    if (lane == 0) mbar_arrive_expect_tx(bar, __popc(have) * 2 * sub * HD);
+    __syncwarp();
+    if (load) {
+      uint8_t* dst = my_stages + st * L::kStageBytes + part * sub * HD;
+      const int y = f.h * c.p.page + (f.now.key0 & (c.p.page - 1));
+      tma_load_3d(dst, &maps.k, bar, 0, y, f.now.id);
+      tma_load_3d(dst + L::kTileBytes, &maps.v, bar, 0, y, f.now.id);
+    }
+    ++fetched;
+  };
+  auto begin_run = [&](long long pos) {
+    f.r = run_at(pos);
+    f.s = seq_tiles(a, f.r.b, false);
+    f.h = f.r.x / p.row_tiles;
+    const int n = f.r.t1 - f.r.t0;
+    f.count = warp < n ? (n - warp + kWarps - 1) / kWarps : 0;
+    f.batch = 0;
+    f.now = look_up(0);
+    for (int k = 0; k < min(f.count, kDepth); ++k) fetch(k);
+    look_up_scales(f.now);
+    f.next = look_up(per_batch);
+    look_up_scales(f.next);
+  };
+
+  {
     const int g = lane >> 2, t4 = lane & 3;
-    const ConsumerSync sync;
-    long long first_tile = 0;  // tiles of this block before the run
-    for (long long pos = begin; pos < end;) {
-      const Run r = run_at(pos);
-      const SeqTiles s = seq_tiles(a, r.b, false);
-      const int h = r.x / p.row_tiles, row0 = (r.x % p.row_tiles) * kRows;
-      const size_t q_base = (static_cast<size_t>(r.b) * a.Hq + static_cast<size_t>(h) * p.group) *
-                                a.Nq + row0;  // of q, out, lse: rows are contiguous
-      // the two rows of this lane: their visible keys, their queries in fp16
-      // scaled by a power of two to at most 2 in magnitude (exact for bf16
-      // unless 2^14 below the row's largest)
-      Range rg[2];
-      bool live[2];
-      float qf[2];  // logits: acc * qf * k_scale
-      uint32_t qa[kSteps][4];
+    const BlockSync sync;
+    uint32_t taken = 0;  // tiles of this warp so far
+    // Queries of a run as the first product's operand, in the merge buffer, which is
+    // free then: lane (g, t) holds row g + 8 nt, in fp16, scaled by a power of two to less
+    // than 2 in magnitude (exact for bf16 values unless they lie 2^14 below the
+    // row's largest). Thread = (row, 1 / 8 of its columns).
+    uint2* const qs = reinterpret_cast<uint2*>(merge);  // [NT][kSteps][32]
+    auto put_queries = [&](const Run& r, const SeqTiles& s, int h) {
+      constexpr int kC = HD / 8;  // 16 or 8 columns a thread: a chunk, or half of one
+      for (int x0 = tid & ~7; x0 < kRows * 8; x0 += kDecodeThreads) {
+        const int rr = x0 >> 3, piece = tid & 7;
+        const int row = (r.x % p.row_tiles) * kRows + rr, i = row % a.Nq;
+        const bool have = row < p.R && i < s.n;
+        float x[kC], top = 0.f;
+        if (have) {
+          const T* src = static_cast<const T*>(a.q) + ((static_cast<size_t>(r.b) * a.Hq +
+              static_cast<size_t>(h) * p.group) * a.Nq + row) * HD + kC * piece;
+          constexpr int kVec = 16 / sizeof(T);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int rr = g + 8 * e, i = (row0 + rr) % a.Nq;
-        live[e] = row0 + rr < p.R && i < s.n;
-        rg[e] = Range{0, 0, 0};
-        if (live[e]) rg[e] = visible_range(a.see, static_cast<long long>(s.L) - s.n + i, s.L);
-        live[e] = live[e] && (rg[e].s > 0 || rg[e].hi > rg[e].lo);
-        float x[kU][16];
-        float top = 0.f;
+          for (int v = 0; v < kC / kVec; ++v) {
+            const uint4 w = reinterpret_cast<const uint4*>(src)[v];
+            const T* el = reinterpret_cast<const T*>(&w);
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-          if (live[e]) {
-            const T* src = static_cast<const T*>(a.q) + (q_base + rr) * HD + 16 * (kU * t4 + u);
-            constexpr int kVec = 16 / sizeof(T);
-#pragma unroll
-            for (int v = 0; v < 16 / kVec; ++v) {
-              const uint4 w = reinterpret_cast<const uint4*>(src)[v];
-              const T* el = reinterpret_cast<const T*>(&w);
-#pragma unroll
-              for (int k = 0; k < kVec; ++k) x[u][v * kVec + k] = load_f32(el + k);
-            }
-          } else {
-#pragma unroll
-            for (int k = 0; k < 16; ++k) x[u][k] = 0.f;
+            for (int k = 0; k < kVec; ++k) x[v * kVec + k] = load_f32(el + k);
           }
+        } else {
 #pragma unroll
-          for (int k = 0; k < 16; ++k) top = fmaxf(top, fabsf(x[u][k]));
+          for (int k = 0; k < kC; ++k) x[k] = 0.f;
         }
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // 2^-exponent(top), within the normal range both ways
+#pragma unroll
+        for (int k = 0; k < kC; ++k) top = fmaxf(top, fabsf(x[k]));
+        const unsigned eight = 0xffu << (lane & 24);
+#pragma unroll
+        for (int w = 1; w < 8; w <<= 1) top = fmaxf(top, __shfl_xor_sync(eight, top, w));
+        // exponent of the row's largest value, so that its power of two is normal both ways
         const int ex = top > 0.f ? min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -100), 100) : 0;
         const float down = __uint_as_float((127 - ex) << 23);
-        qf[e] = a.sc * __uint_as_float((127 + ex) << 23);
+        const int nt = rr >> 3, to = (rr & 7) * 4;
 #pragma unroll
-        for (int u = 0; u < kU; ++u)
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            qa[4 * u + w][e] = pack_f16x2(x[u][4 * w] * down, x[u][4 * w + 1] * down);
-            qa[4 * u + w][2 + e] = pack_f16x2(x[u][4 * w + 2] * down, x[u][4 * w + 3] * down);
-          }
+        for (int k = 0; k < kC; k += 4) {
+          // columns 16 c + 4 w .. of chunk c = kU t + u are step 4 u + w of lane t
+          const int col = kC * piece + k, chunk = col >> 4, w = (col >> 2) & 3;
+          const int t = chunk / kU, step = 4 * (chunk % kU) + w;
+          qs[(nt * kSteps + step) * 32 + to + t] =
+              make_uint2(pack_f16x2(x[k] * down, x[k + 1] * down),
+                         pack_f16x2(x[k + 2] * down, x[k + 3] * down));
+        }
+        if (piece == 0) {
+          Range rg = {0, 0, 0};
+          if (have) rg = visible_range(a.see, static_cast<long long>(s.L) - s.n + i, s.L);
+          const bool on = rg.s > 0 || rg.hi > rg.lo;
+          ms.range[rr] = rg;
+          ms.live[rr] = on;
+          ms.valid[rr] = have;
+          ms.q_scale[rr] = a.sc * __uint_as_float((127 + ex) << 23);
+        }
       }
-      float m[2] = {-INFINITY, -INFINITY}, M[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-      bool seen[2] = {false, false};
-      float o[kNd][4];
+    };
+    begin_run(begin);
+    put_queries(f.r, f.s, f.h);
+    sync();
+    for (long long pos = begin; pos < end;) {
+      const Run r = f.r;
+      const SeqTiles s = f.s;
+      const int h = f.h, row0 = (r.x % p.row_tiles) * kRows;
+      const size_t q_base = (static_cast<size_t>(r.b) * a.Hq + static_cast<size_t>(h) * p.group) *
+                                a.Nq + row0;  // of q, out, lse: rows are contiguous
+      float qf[NT][2];   // rows 2 t + e + 8 nt of this lane: logit = accumulator * qf * k_scale
+      bool live[NT][2];
+      // a tile that starts at key `from` or later and ends by `to` is seen whole by all rows
+      int from = 0, to = 0x7fffffff;
 #pragma unroll
-      for (int nd = 0; nd < kNd; ++nd)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[nd][e] = 0.f;
-
-      const int n_tiles = r.t1 - r.t0;
-      for (int e0 = (warp + kWarps - static_cast<int>(first_tile % kWarps)) % kWarps; e0 < n_tiles;
-           e0 += kWarps) {
-        const long long nth = first_tile + e0;
-        const int st = static_cast<int>(nth % L::kStages);
-        const bool got = mbar_wait(&ms.full[st], static_cast<uint32_t>(nth / L::kStages) & 1u, abort);
-        if (!__all_sync(0xffffffffu, got)) continue;  // aborted: the status word says so
-        const uint8_t* ks8 = smem + L::stage_off + st * L::kStageBytes;
-        const uint8_t* vs8 = ks8 + L::kTileBytes;
-        const int k0 = s.start(r.t0 + e0);
-        // ---- x = q . k: 8 groups of 8 keys ----
-        float acc[8][4];
-#pragma unroll
-        for (int kn = 0; kn < 8; ++kn) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[kn][e] = 0.f;
-          const int key = kn * 8 + g;
-          uint4 kw[kU];
-#pragma unroll
-          for (int u = 0; u < kU; ++u) {
-            const int chunk = kU == 2 ? ((2 * t4 + u) ^ (key & 7)) : (t4 ^ ((key >> 1) & 3));
-            kw[u] = *reinterpret_cast<const uint4*>(ks8 + key * HD + chunk * 16);
+        for (int e = 0; e < 2; ++e) {
+          const int rr = 2 * t4 + e + 8 * nt;
+          qf[nt][e] = ms.q_scale[rr];
+          live[nt][e] = ms.live[rr];
+          const Range rg = ms.range[rr];
+          if (live[nt][e]) {
+            from = max(from, rg.s == rg.lo ? 0 : rg.lo);
+            to = min(to, rg.hi);
           }
+        }
+#pragma unroll
+      for (int w = 1; w < 4; w <<= 1) {
+        from = max(from, __shfl_xor_sync(0xffffffffu, from, w));
+        to = min(to, __shfl_xor_sync(0xffffffffu, to, w));
+      }
+      float m[NT][2], M[NT][2], l[NT][2], af[NT][2];
+      bool seen[NT][2];
+      float o[kSteps][NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          m[nt][e] = M[nt][e] = -INFINITY;
+          l[nt][e] = 0.f;
+          seen[nt][e] = false;
+        }
+#pragma unroll
+        for (int mt = 0; mt < kSteps; ++mt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[mt][nt][e] = 0.f;
+      }
+
+      const int n_tiles = r.t1 - r.t0, count = f.count;
+      for (int kth = 0; kth < count; ++kth, ++taken) {
+        const int st = taken % kDepth;
+        const bool got = mbar_wait(&ms.full[warp][st], (taken / kDepth) & 1u, abort);
+        if (!__all_sync(0xffffffffu, got)) continue;  // aborted: the status word says so
+        const uint8_t* ks8 = my_stages + st * L::kStageBytes;
+        const uint8_t* vs8 = ks8 + L::kTileBytes;
+        const int k0 = s.start(r.t0 + warp + kth * kWarps);
+        // ---- x = k . q, 16 keys at a time ----
+        float acc[kKt][NT][4];
+#pragma unroll
+        for (int kt = 0; kt < kKt; ++kt) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[kt][nt][e] = 0.f;
+          uint2 qw[NT][kSteps];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int x = 0; x < kSteps; ++x) qw[nt][x] = qs[(nt * kSteps + x) * 32 + lane];
+          uint4 kw[2][kU];
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+              const int key = kt * 16 + x * 8 + g;
+              const int chunk = kU == 2 ? ((2 * t4 + u) ^ (key & 7)) : (t4 ^ ((key >> 1) & 3));
+              kw[x][u] = *reinterpret_cast<const uint4*>(ks8 + key * HD + chunk * 16);
+            }
 #pragma unroll
           for (int u = 0; u < kU; ++u) {
-            const uint32_t w[4] = {kw[u].x, kw[u].y, kw[u].z, kw[u].w};
+            const uint32_t w0[4] = {kw[0][u].x, kw[0][u].y, kw[0][u].z, kw[0][u].w};
+            const uint32_t w1[4] = {kw[1][u].x, kw[1][u].y, kw[1][u].z, kw[1][u].w};
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-              mma16816(acc[kn], qa[4 * u + x], e4m3x2_to_f16x2(w[x]), e4m3x2_to_f16x2(w[x] >> 16));
+            for (int x = 0; x < 4; ++x) {
+              const uint32_t ka[4] = {e4m3x2_to_f16x2(w0[x]), e4m3x2_to_f16x2(w1[x]),
+                                      e4m3x2_to_f16x2(w0[x] >> 16), e4m3x2_to_f16x2(w1[x] >> 16)};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma16816(acc[kt][nt], ka, qw[nt][4 * u + x].x, qw[nt][4 * u + x].y);
+            }
           }
         }
         // ---- logits, masks, maxima ----
-        bool whole = true, pages = true;
+        float ks[kKt], lv[kKt];
+        bool whole = true;
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          whole = whole && (!live[e] || (k0 + kTile <= rg[e].s) ||
-                            (rg[e].lo <= k0 && k0 + kTile <= rg[e].hi) ||
-                            (rg[e].s == rg[e].lo && k0 + kTile <= rg[e].hi));
-        const int spp = kTile / p.sub_rows;
-        for (int x = 0; x < spp; ++x) pages = pages && !(ms.k_scale[st][x] < 0.f);
-        const bool plain = __all_sync(0xffffffffu, whole) && pages;
-        float tm[2] = {-INFINITY, -INFINITY}, tM[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-        for (int kn = 0; kn < 8; ++kn) {
-          const int sp = (kn * 8) / p.sub_rows;
-          const float ks = ms.k_scale[st][sp], lv = ms.v_log2[st][sp];
-          const float f[2] = {qf[0] * ks, qf[1] * ks};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float x = acc[kn][e] * f[e >> 1];
-            if (!plain) {
-              const int key = k0 + kn * 8 + 2 * t4 + (e & 1);
-              const Range& rr = rg[e >> 1];
-              if (ks < 0.f || !(key < rr.s || (key >= rr.lo && key < rr.hi))) x = -INFINITY;
-              else seen[e >> 1] = true;
-            }
-            acc[kn][e] = x;
-            tm[e >> 1] = fmaxf(tm[e >> 1], x);
-            tM[e >> 1] = fmaxf(tM[e >> 1], x + lv);
-          }
+        for (int kt = 0; kt < kKt; ++kt) {
+          const int from = (kth - f.batch) * spp + ((kt * 16) >> sub_shift);
+          ks[kt] = __shfl_sync(0xffffffffu, from >= 0 ? f.now.ks : f.ks0, from & 31);
+          lv[kt] = log2_of_scale(__shfl_sync(0xffffffffu, from >= 0 ? f.now.vs : f.vs0, from & 31));
+          whole = whole && !(ks[kt] < 0.f);
         }
-        if (plain) seen[0] = seen[1] = true;
-        float nm[2], nM[2];  // references, 0 where nothing has been seen
+        // one scale for all values of the tile: the two maxima differ by it
+        bool one_scale = true;
+#pragma unroll
+        for (int kt = 1; kt < kKt; ++kt) one_scale = one_scale && lv[kt] == lv[0];
+        const bool plain = whole && k0 >= from && k0 + kTile <= to;  // the same in the whole warp
         bool moved = false;
+        float nm[NT][2], nM[NT][2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          tm[e] = fmaxf(tm[e], __shfl_xor_sync(0xffffffffu, tm[e], 1));
-          tm[e] = fmaxf(tm[e], __shfl_xor_sync(0xffffffffu, tm[e], 2));
-          tM[e] = fmaxf(tM[e], __shfl_xor_sync(0xffffffffu, tM[e], 1));
-          tM[e] = fmaxf(tM[e], __shfl_xor_sync(0xffffffffu, tM[e], 2));
-          const float mn = fmaxf(m[e], tm[e]), Mn = fmaxf(M[e], tM[e]);
-          l[e] *= m[e] == -INFINITY ? 0.f : exp2f(m[e] - mn);
-          moved = moved || Mn != M[e];
-          tM[e] = M[e] == -INFINITY ? 0.f : exp2f(M[e] - Mn);  // factor of the accumulator
-          m[e] = mn;
-          M[e] = Mn;
-          nm[e] = mn == -INFINITY ? 0.f : mn;
-          nM[e] = Mn == -INFINITY ? 0.f : Mn;
-        }
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float tm = -INFINITY, tM = -INFINITY;
+#pragma unroll
+            for (int kt = 0; kt < kKt; ++kt)
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                float v = acc[kt][nt][2 * x + e] * (qf[nt][e] * ks[kt]);
+                if (!plain) {
+                  const int key = k0 + kt * 16 + x * 8 + g;
+                  const Range rr = ms.range[2 * t4 + e + 8 * nt];
+                  if (ks[kt] < 0.f || !(key < rr.s || (key >= rr.lo && key < rr.hi))) v = -INFINITY;
+                  else seen[nt][e] = true;
+                }
+                acc[kt][nt][2 * x + e] = v;
+                tm = fmaxf(tm, v);
+                if (!one_scale) tM = fmaxf(tM, v + lv[kt]);
+              }
+            if (plain) seen[nt][e] = true;
+#pragma unroll
+            for (int w = 4; w < 32; w <<= 1) {
+              tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, w));
+              if (!one_scale) tM = fmaxf(tM, __shfl_xor_sync(0xffffffffu, tM, w));
+            }
+            if (one_scale) tM = tm + lv[0];
+            const float mn = fmaxf(m[nt][e], tm), Mn = fmaxf(M[nt][e], tM);
+            // -inf - -inf only where nothing has been seen: the sums are 0 then
+            nm[nt][e] = mn == -INFINITY ? 0.f : mn;
+            nM[nt][e] = Mn == -INFINITY ? 0.f : Mn;
+            l[nt][e] *= ex2_approx(m[nt][e] - nm[nt][e]);
+            af[nt][e] = ex2_approx(M[nt][e] - nM[nt][e]);
+            moved = moved || Mn != M[nt][e];
+            m[nt][e] = mn;
+            M[nt][e] = Mn;
+          }
         if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-          for (int nd = 0; nd < kNd; ++nd) {
-            o[nd][0] *= tM[0];
-            o[nd][1] *= tM[0];
-            o[nd][2] *= tM[1];
-            o[nd][3] *= tM[1];
-          }
+          for (int mt = 0; mt < kSteps; ++mt)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[mt][nt][e] *= af[nt][e & 1];
         }
         // ---- weights and the second product, 16 keys at a time ----
 #pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk) {
-          const float lv = ms.v_log2[st][(kk * 16) / p.sub_rows];
-          const float sh[2] = {lv - nM[0], lv - nM[1]};
-          uint32_t pa[4];
+        for (int kt = 0; kt < kKt; ++kt) {
+          uint32_t pb[NT][2];
 #pragma unroll
-          for (int half = 0; half < 2; ++half)
+          for (int nt = 0; nt < NT; ++nt) {
+            const float sh[2] = {lv[kt] - nM[nt][0], lv[kt] - nM[nt][1]};
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float x0 = acc[2 * kk + half][2 * e], x1 = acc[2 * kk + half][2 * e + 1];
-              l[e] += ex2_approx(x0 - nm[e]) + ex2_approx(x1 - nm[e]);
-              pa[2 * half + e] = pack_f16x2(ex2_approx(x0 + sh[e]), ex2_approx(x1 + sh[e]));
+            for (int x = 0; x < 2; ++x) {
+              const float v0 = acc[kt][nt][2 * x], v1 = acc[kt][nt][2 * x + 1];
+              l[nt][0] += ex2_approx(v0 - nm[nt][0]);
+              l[nt][1] += ex2_approx(v1 - nm[nt][1]);
+              pb[nt][x] = transpose8x8(pack_f16x2(ex2_approx(v0 + sh[0]), ex2_approx(v1 + sh[1])));
             }
-          uint32_t vw[4][kNd / 4];  // keys 2t, 2t+1, 2t+8, 2t+9: HD / 8 bytes of each
+          }
+          constexpr int kW = HD / 32;  // words of a value per lane
+          uint32_t vw[4][kW];          // keys 2t, 2t+1, 2t+8, 2t+9: HD / 8 bytes of each
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int key = kk * 16 + 2 * t4 + (e & 1) + (e >> 1) * 8;
+            const int key = kt * 16 + 2 * t4 + (e & 1) + (e >> 1) * 8;
             if (HD == 128) {
               const uint4 v = *reinterpret_cast<const uint4*>(vs8 + key * HD + (g ^ (key & 7)) * 16);
               vw[e][0] = v.x;
               vw[e][1] = v.y;
-              vw[e][kNd / 4 - 2] = v.z;
-              vw[e][kNd / 4 - 1] = v.w;
+              vw[e][kW - 2] = v.z;
+              vw[e][kW - 1] = v.w;
             } else {
               const uint2 v = *reinterpret_cast<const uint2*>(
                   vs8 + key * HD + ((g >> 1) ^ ((key >> 1) & 3)) * 16 + (g & 1) * 8);
@@ -538,106 +634,142 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
             if (!plain) {
               // a value that no row sees may be anything, also NaN
               const int kx = k0 + key;
-              if (ms.k_scale[st][(kk * 16) / p.sub_rows] < 0.f ||
-                  !(kx < s.SA || (kx >= s.LB && kx < s.HB)))
+              if (ks[kt] < 0.f || !(kx < s.SA || (kx >= s.LB && kx < s.HB)))
 #pragma unroll
-                for (int w = 0; w < kNd / 4; ++w) vw[e][w] = 0u;
+                for (int w = 0; w < kW; ++w) vw[e][w] = 0u;
             }
           }
 #pragma unroll
-          for (int w = 0; w < kNd / 4; ++w) {
-            const uint32_t a_lo = __byte_perm(vw[0][w], vw[1][w], 0x5140);
-            const uint32_t a_hi = __byte_perm(vw[0][w], vw[1][w], 0x7362);
-            const uint32_t b_lo = __byte_perm(vw[2][w], vw[3][w], 0x5140);
-            const uint32_t b_hi = __byte_perm(vw[2][w], vw[3][w], 0x7362);
-            mma16816(o[4 * w], pa, e4m3x2_to_f16x2(a_lo), e4m3x2_to_f16x2(b_lo));
-            mma16816(o[4 * w + 1], pa, e4m3x2_to_f16x2(a_lo >> 16), e4m3x2_to_f16x2(b_lo >> 16));
-            mma16816(o[4 * w + 2], pa, e4m3x2_to_f16x2(a_hi), e4m3x2_to_f16x2(b_hi));
-            mma16816(o[4 * w + 3], pa, e4m3x2_to_f16x2(a_hi >> 16), e4m3x2_to_f16x2(b_hi >> 16));
+          for (int w = 0; w < kW; ++w) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const uint32_t lo = __byte_perm(vw[0][w], vw[1][w], x ? 0x7362 : 0x5140);
+              const uint32_t hi = __byte_perm(vw[2][w], vw[3][w], x ? 0x7362 : 0x5140);
+              const uint32_t va[4] = {e4m3x2_to_f16x2(lo), e4m3x2_to_f16x2(lo >> 16),
+                                      e4m3x2_to_f16x2(hi), e4m3x2_to_f16x2(hi >> 16)};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma16816(o[2 * w + x][nt], va, pb[nt][0], pb[nt][1]);
+            }
           }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ms.empty[st]);
+        if (kth + kDepth < count) fetch(kth + kDepth);
       }
-      // ---- merge of the warps ----
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
-        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
-        int sn = seen[e];
-        sn |= __shfl_xor_sync(0xffffffffu, sn, 1);
-        sn |= __shfl_xor_sync(0xffffffffu, sn, 2);
-        if (t4 == 0) {
-          ms.m[warp][g + 8 * e] = m[e];
-          ms.M[warp][g + 8 * e] = M[e];
-          ms.l[warp][g + 8 * e] = l[e];
-          ms.seen[warp][g + 8 * e] = sn;
-        }
-      }
-      sync();
-      float gm[2], gM[2], gl[2];
-      bool gs[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        gm[e] = gM[e] = -INFINITY;
-        gs[e] = false;
-        for (int w = 0; w < kWarps; ++w) {
-          gm[e] = fmaxf(gm[e], ms.m[w][g + 8 * e]);
-          gM[e] = fmaxf(gM[e], ms.M[w][g + 8 * e]);
-          gs[e] = gs[e] || ms.seen[w][g + 8 * e];
-        }
-        gl[e] = 0.f;
-        for (int w = 0; w < kWarps; ++w) {
-          const float mw = ms.m[w][g + 8 * e], lw = ms.l[w][g + 8 * e];
-          if (mw != -INFINITY) gl[e] += lw * exp2f(mw - gm[e]);
-          else if (!(lw == 0.f)) gl[e] = lw;  // NaN
-        }
-      }
-      {
-        const float f[2] = {M[0] == -INFINITY ? 0.f : exp2f(M[0] - gM[0]),
-                            M[1] == -INFINITY ? 0.f : exp2f(M[1] - gM[1])};
-#pragma unroll
-        for (int nd = 0; nd < kNd; ++nd)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            merge[(warp * (HD / 2) + nd * 4 + e) * 32 + lane] = o[nd][e] * f[e >> 1];
-      }
-      sync();
-      // this warp sums column tiles kPer warp ..: columns (HD / 8) (2 t) + nd and (HD / 8) (2 t + 1) + nd
-      constexpr int kPer = kNd / kWarps;  // 2 or 1
       const bool full_unit = n_tiles == s.T;
       const size_t slot = static_cast<size_t>(r.b) * p.units_seq + r.x + blockIdx.x;
+      pos += n_tiles;
+      if (pos < end) begin_run(pos);
+      // ---- merge of the warps; those without a tile hold -inf, 0 ----
+      const int used = min(n_tiles, kWarps);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int rr = g + 8 * e, i = (row0 + rr) % a.Nq;
-        const bool valid = row0 + rr < p.R && i < s.n;
-        const float inv = live[e] && gl[e] > 0.f ? exp2f(gM[e] - gm[e]) / gl[e] : 0.f;
-        const float lse = live[e] && gl[e] > 0.f ? gm[e] + log2f(gl[e]) : -INFINITY;
-        bool finite = true;
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-          const int nd = warp * kPer + k;
+        for (int e = 0; e < 2; ++e) {
+          int sn = seen[nt][e];
 #pragma unroll
-          for (int z = 0; z < 2; ++z) {
-            float x = 0.f;
-            for (int w = 0; w < kWarps; ++w)
-              x += merge[(w * (HD / 2) + nd * 4 + 2 * e + z) * 32 + lane];
-            x = live[e] ? x * inv : 0.f;
-            finite = finite && fabsf(x) < INFINITY;
-            const int col = (HD / 8) * (2 * t4 + z) + nd;
-            if (full_unit) {
-              if (valid) store_f32(static_cast<T*>(a.out) + (q_base + rr) * HD + col, x);
-            } else {
-              p.opart[(slot * kRows + rr) * HD + col] = x;
-            }
+          for (int w = 4; w < 32; w <<= 1) {
+            l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], w);
+            sn |= __shfl_xor_sync(0xffffffffu, sn, w);
+          }
+          if (g == 0) {
+            const int rr = 2 * t4 + e + 8 * nt;
+            ms.m[warp][rr] = m[nt][e];
+            ms.M[warp][rr] = M[nt][e];
+            ms.l[warp][rr] = l[nt][e];
+            ms.seen[warp][rr] = sn;
           }
         }
-        if (warp == 0 && t4 == 0) {
-          if (!full_unit) p.lpart[slot * kRows + rr] = lse;
-          else if (valid && a.lse) a.lse[q_base + rr] = lse * kLn2F;
+      sync();
+      float inv[NT][2];
+      bool on[NT][2];  // rows that saw a key of this run
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int rr = 2 * t4 + e + 8 * nt;
+          float gm = -INFINITY, gM = -INFINITY, gl = 0.f;
+          int sn = 0;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) {
+            gm = fmaxf(gm, ms.m[w][rr]);
+            gM = fmaxf(gM, ms.M[w][rr]);
+            sn |= ms.seen[w][rr];
+          }
+          const float zm = gm == -INFINITY ? 0.f : gm, zM = gM == -INFINITY ? 0.f : gM;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) {
+            const float mw = ms.m[w][rr], lw = ms.l[w][rr];
+            gl += mw == -INFINITY ? lw : lw * ex2_approx(mw - zm);  // without a maximum: 0 or NaN
+          }
+          on[nt][e] = live[nt][e] && sn;
+          const bool fine = gl > 0.f && gl < INFINITY;
+          inv[nt][e] = on[nt][e] && fine ? exp2f(zM - zm) / gl : 0.f;
+          const float lse = on[nt][e] && fine ? gm + log2f(gl) : -INFINITY;
+          af[nt][e] = ex2_approx(M[nt][e] - zM);
+          if (warp == 0 && g == 0) {
+            if (on[nt][e] && !fine) atomicOr(&ms.flags, 1u << rr);
+            if (!full_unit) p.lpart[slot * kRows + rr] = lse;
+            else if (a.lse && ms.valid[rr]) a.lse[q_base + rr] = lse * kLn2F;
+          }
         }
-        if (live[e] && gs[e] && (!finite || !(gl[e] > 0.f) || !(gl[e] < INFINITY)))
-          atomicOr(&ms.flags, 1u << rr);
+      // the accumulators go through shared memory kMergeWarps warps at a time
+      constexpr int kMw = L::kMergeWarps;
+#pragma unroll
+      for (int mt = 0; mt < kSteps; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[mt][nt][e] *= af[nt][e & 1];
+      for (int w0 = 0; w0 < used; w0 += kMw) {
+        if (w0 > 0) sync();
+        if (warp >= w0 && warp < min(w0 + kMw, used)) {
+          float* to = merge + (warp - w0) * L::kRegs * 32 + lane;
+#pragma unroll
+          for (int mt = 0; mt < kSteps; ++mt)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                float& x = to[((mt * NT + nt) * 4 + e) * 32];
+                x = w0 > 0 ? x + o[mt][nt][e] : o[mt][nt][e];
+              }
+        }
+      }
+      sync();
+      // accumulators (mt, nt, e) and (mt, nt, e + 2) of lane (g, t), e < 2, are columns
+      // (HD / 8) g + 2 mt and the next of row 2 t + e + 8 nt; the warps share them out
+      const int summed = min(used, kMw);
+#pragma unroll
+      for (int j0 = 0; j0 < L::kRegs / 2; j0 += kWarps) {
+        const int j = j0 + warp;
+        if (j < L::kRegs / 2) {
+          const int e = j & 1, nt = (j >> 1) % NT, mt = j / (2 * NT);
+          const float* from = merge + ((mt * NT + nt) * 4 + e) * 32 + lane;
+          float x0 = 0.f, x1 = 0.f;
+#pragma unroll
+          for (int w = 0; w < kMw; ++w)
+            if (w < summed) {
+              x0 += from[w * L::kRegs * 32];
+              x1 += from[w * L::kRegs * 32 + 64];
+            }
+          const int rr = 2 * t4 + e + 8 * nt, col = (HD / 8) * g + 2 * mt;
+          const float iv = NT == 1 ? (e ? inv[0][1] : inv[0][0])
+                                   : nt ? (e ? inv[NT - 1][1] : inv[NT - 1][0])
+                                        : (e ? inv[0][1] : inv[0][0]);
+          const bool here = NT == 1 ? (e ? on[0][1] : on[0][0])
+                                    : nt ? (e ? on[NT - 1][1] : on[NT - 1][0])
+                                         : (e ? on[0][1] : on[0][0]);
+          x0 = here ? x0 * iv : 0.f;
+          x1 = here ? x1 * iv : 0.f;
+          if (here && !(fabsf(x0) < INFINITY && fabsf(x1) < INFINITY)) atomicOr(&ms.flags, 1u << rr);
+          if (!full_unit) {
+            *reinterpret_cast<float2*>(p.opart + (slot * kRows + rr) * HD + col) = make_float2(x0, x1);
+          } else if (ms.valid[rr]) {
+            T* dst = static_cast<T*>(a.out) + (q_base + rr) * HD + col;
+            store_f32(dst, x0);
+            store_f32(dst + 1, x1);
+          }
+        }
       }
       sync();
       // Rows whose result is not finite are taken again by the definition (a value
@@ -648,11 +780,11 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         todo &= todo - 1;
         const PagedKV<HD> kv = {c, c.c.table + static_cast<size_t>(r.b) * c.p.max_pages, h, s, r.t0,
                                 r.t1};
-        for (int x = tid; x < HD; x += kConsumers)
+        for (int x = tid; x < HD; x += kDecodeThreads)
           ms.q[x] = load_f32(static_cast<const T*>(a.q) + (q_base + rr) * HD + x);
         sync();
         float lm, ll, lo;
-        literal_row<kConsumers, HD>(
+        literal_row<kDecodeThreads, HD>(
             kv, ms.q, visible_range(a.see, static_cast<long long>(s.L) - s.n + i, s.L), a.sc,
             scratch, sync, lm, ll, lo);
         const float inv = ll == 0.f ? 0.f : 1.f / ll;
@@ -667,9 +799,17 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         }
         sync();
       }
-      if (tid == 0) ms.flags = 0;  // read by all before; set again after the next merge's barriers
-      first_tile += n_tiles;
-      pos += n_tiles;
+      if (tid == 0) ms.flags = 0;  // all have read it; set again only behind the next barrier
+      if (pos < end) {
+        put_queries(f.r, f.s, f.h);
+        sync();
+      }
+    }
+    // let the copies in flight land (there are none unless the block aborted)
+    if (lane == 0) {
+      volatile int never = 0;
+      for (uint32_t n = fetched > kDepth ? fetched - kDepth : 0; n < fetched; ++n)
+        mbar_wait(&ms.full[warp][n % kDepth], (n / kDepth) & 1u, &never);
     }
   }
   __syncthreads();
@@ -677,48 +817,54 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
 }
 
 // Joins the partial results of units that more than one block worked on, in the
-// order of the blocks, and writes the rows that see nothing. One block per
-// (sequence, unit); thread = (row, 8 columns).
-template <int HD, typename T>
-__global__ void __launch_bounds__(kRows* HD / 8) cache_combine_kernel(const DecodeParams p) {
+// order of the blocks, and writes the rows that see nothing. A warp per query
+// row: the lanes take one block's log-sum-exp each, then HD / 32 columns each.
+template <int HD, int NT, typename T>
+__global__ void __launch_bounds__(NT* 256) cache_combine_kernel(const DecodeParams p) {
+  constexpr int kRows = 8 * NT, kC = HD / 32;
   const CacheAttnArgs& a = p.a;
   const int b = blockIdx.x / p.units_seq, x = blockIdx.x % p.units_seq;
-  const long long before = p.pre[b], tiles = p.pre[b + 1] - before;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // all of the decode kernel's writes
+  const int before = p.pre[b], tiles = p.pre[b + 1] - before, all = p.pre[a.cache.p.B];
   const int h = x / p.row_tiles, row0 = (x % p.row_tiles) * kRows;
-  const int rr = threadIdx.x / (HD / 8), col = (threadIdx.x % (HD / 8)) * 8;
+  const int rr = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n = clamp_count(a.n_q, b, a.Nq, a.Nq, a.cache.stats, false);
-  const bool valid = row0 + rr < p.R && (row0 + rr) % a.Nq < n;
+  if (row0 + rr >= p.R || (row0 + rr) % a.Nq >= n) return;
   const size_t row = (static_cast<size_t>(b) * a.Hq + static_cast<size_t>(h) * p.group) * a.Nq +
                      row0 + rr;
-  T* out = static_cast<T*>(a.out) + row * HD + col;
-  float num[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  float num[kC] = {};
   float lse = -INFINITY, inv = 0.f;
   if (tiles > 0) {
-    const long long total = static_cast<long long>(p.pre[a.cache.p.B]) * p.units_seq;
+    const long long total = static_cast<long long>(all) * p.units_seq;
     const int blocks = blocks_for(total);
-    const long long at = before * p.units_seq + x * tiles;
+    const long long at = static_cast<long long>(before) * p.units_seq + static_cast<long long>(x) * tiles;
     const int c0 = owner(at, total, blocks), c1 = owner(at + tiles - 1, total, blocks);
     if (c0 == c1) return;  // written whole
+    const size_t slot0 = (static_cast<size_t>(blockIdx.x) + c0) * kRows + rr;
+    const int count = c1 - c0 + 1;
     float M = -INFINITY, den = 0.f;
     bool nan = false;
-    for (int c = c0; c <= c1; ++c) {
-      const float l = p.lpart[(static_cast<size_t>(blockIdx.x) + c) * kRows + rr];
+    for (int i = lane; i < count; i += 32) {
+      const float l = p.lpart[slot0 + static_cast<size_t>(i) * kRows];
       M = fmaxf(M, l);
       nan = nan || l != l;
     }
-    for (int c = c0; c <= c1; ++c) {
-      const size_t slot = (static_cast<size_t>(blockIdx.x) + c) * kRows + rr;
-      const float l = p.lpart[slot];
-      if (l == -INFINITY) continue;
-      const float w = exp2f(l - M);
-      den += w;
 #pragma unroll
-      for (int e = 0; e < 8; e += 4) {
-        const float4 o = *reinterpret_cast<const float4*>(p.opart + slot * HD + col + e);
-        num[e] = fmaf(w, o.x, num[e]);
-        num[e + 1] = fmaf(w, o.y, num[e + 1]);
-        num[e + 2] = fmaf(w, o.z, num[e + 2]);
-        num[e + 3] = fmaf(w, o.w, num[e + 3]);
+    for (int w = 16; w > 0; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
+    nan = __any_sync(0xffffffffu, nan);
+    const float zM = M == -INFINITY ? 0.f : M;
+    for (int i0 = 0; i0 < count; i0 += 32) {
+      float w = 0.f;
+      if (i0 + lane < count) w = exp2f(p.lpart[slot0 + static_cast<size_t>(i0 + lane) * kRows] - zM);
+      const int m = min(32, count - i0);
+#pragma unroll 4
+      for (int i = 0; i < m; ++i) {
+        const float wi = __shfl_sync(0xffffffffu, w, i);
+        const float* o = p.opart + (slot0 + static_cast<size_t>(i0 + i) * kRows) * HD + lane * kC;
+        den += wi;
+        // a part that holds none of the row's keys is 0
+#pragma unroll
+        for (int e = 0; e < kC; ++e) num[e] = fmaf(wi, o[e], num[e]);
       }
     }
     if (den > 0.f || nan) {
@@ -726,10 +872,10 @@ __global__ void __launch_bounds__(kRows* HD / 8) cache_combine_kernel(const Deco
       lse = nan ? den : M + log2f(den);
     }
   }
-  if (!valid) return;
+  T* out = static_cast<T*>(a.out) + row * HD + lane * kC;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) store_f32(out + e, num[e] * inv);
-  if (a.lse && col == 0) a.lse[row] = lse * kLn2F;
+  for (int e = 0; e < kC; ++e) store_f32(out + e, num[e] * inv);
+  if (a.lse && lane == 0) a.lse[row] = lse * kLn2F;
 }
 
 // [n_pages, Hkv * page, HD] bytes, swizzled over the whole row
@@ -749,15 +895,30 @@ bool make_page_map(CUtensorMap* m, const void* base, const sparsepr_cache_params
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int HD, typename T>
+template <int HD, int NT, typename T>
 cudaError_t launch_decode(const DecodeParams& p, const DecodeMaps& maps, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(cache_decode_kernel<HD, T>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       DecodeSmem<HD>::bytes);
+  constexpr int kBytes = DecodeSmem<HD, NT>::bytes;
+  cudaError_t e = cudaFuncSetAttribute(cache_decode_kernel<HD, NT, T>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
   if (e != cudaSuccess) return e;
-  cache_decode_kernel<HD, T><<<kDecodeBlocks, kDecodeThreads, DecodeSmem<HD>::bytes, st>>>(maps, p);
-  cache_combine_kernel<HD, T><<<p.a.cache.p.B * p.units_seq, kRows * HD / 8, 0, st>>>(p);
-  return cudaGetLastError();
+  cache_decode_kernel<HD, NT, T><<<kDecodeBlocks, kDecodeThreads, kBytes, st>>>(maps, p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // launched beside the tail of the decode kernel (programmatic dependent launch)
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.a.cache.p.B * p.units_seq);
+  cfg.blockDim = dim3(NT * 256);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cache_combine_kernel<HD, NT, T>, p);
+}
+template <int HD, typename T>
+cudaError_t launch_decode_rows(const DecodeParams& p, const DecodeMaps& maps, cudaStream_t st) {
+  return p.rows == 8 ? launch_decode<HD, 1, T>(p, maps, st) : launch_decode<HD, 2, T>(p, maps, st);
 }
 
 }  // namespace
@@ -765,9 +926,9 @@ cudaError_t launch_decode(const DecodeParams& p, const DecodeMaps& maps, cudaStr
 CacheAttnPlan cache_attn_plan(const sparsepr_cache_params& p, int Hq, int Nq) {
   CacheAttnPlan w = {};
   const int R = Hq / p.Hkv * Nq;
-  w.row_tiles = (R + kRows - 1) / kRows;
+  w.rows = R <= 8 ? 8 : 16;
+  w.row_tiles = (R + w.rows - 1) / w.rows;
   w.slots = static_cast<size_t>(p.B) * p.Hkv * w.row_tiles + kDecodeBlocks;
-  w.slot_rows = kRows;
   return w;
 }
 
@@ -778,9 +939,10 @@ cudaError_t launch_cache_attention(const CacheAttnArgs& a, cudaStream_t st) {
   p.a = a;
   p.group = a.Hq / a.cache.p.Hkv;
   p.R = p.group * a.Nq;
+  p.rows = w.rows;
   p.row_tiles = w.row_tiles;
   p.units_seq = a.cache.p.Hkv * w.row_tiles;
-  p.sub_rows = a.cache.p.page < kTile ? a.cache.p.page : kTile;
+  p.sub_rows = min(a.cache.p.page, tile_keys(a.cache.p.d));
   p.pre = a.pre;
   p.opart = a.opart;
   p.lpart = a.lpart;
@@ -791,10 +953,10 @@ cudaError_t launch_cache_attention(const CacheAttnArgs& a, cudaStream_t st) {
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if (a.bf16)
-    return a.cache.p.d == 128 ? launch_decode<128, __nv_bfloat16>(p, maps, st)
-                              : launch_decode<64, __nv_bfloat16>(p, maps, st);
-  return a.cache.p.d == 128 ? launch_decode<128, float>(p, maps, st)
-                            : launch_decode<64, float>(p, maps, st);
+    return a.cache.p.d == 128 ? launch_decode_rows<128, __nv_bfloat16>(p, maps, st)
+                              : launch_decode_rows<64, __nv_bfloat16>(p, maps, st);
+  return a.cache.p.d == 128 ? launch_decode_rows<128, float>(p, maps, st)
+                            : launch_decode_rows<64, float>(p, maps, st);
 }
 
 }  // namespace spr

@@ -368,9 +368,9 @@ struct CacheAttnArgs {
   float *opart, *lpart;  // partial outputs and log2-sum-exps of units cut over blocks
 };
 struct CacheAttnPlan {
-  int row_tiles;   // tiles of query rows per key head
-  size_t slots;    // partial results
-  int slot_rows;   // rows of each
+  int rows;       // query rows of a unit
+  int row_tiles;  // units per key head
+  size_t slots;   // partial results of `rows` rows
 };
 CacheAttnPlan cache_attn_plan(const sparsepr_cache_params& p, int Hq, int Nq);
 cudaError_t launch_cache_attention(const CacheAttnArgs& a, cudaStream_t st);

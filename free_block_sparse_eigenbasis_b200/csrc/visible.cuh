@@ -18,11 +18,14 @@ struct Range {
 // Keys that the query at position p of a sequence of L keys sees. All three
 // ends grow with p, so the keys of a run of rows lie in [0, s of the last row)
 // and [lo of the first, hi of the last).
+// Positions and counts are below 2^31; only the products by the frame need
+// more, and divisions stay in 32 bits.
 __host__ __device__ inline Range visible_range(const sparsepr_visibility& see, long long p,
                                                long long L) {
   Range r = {0, 0, 0};
   if (p < 0 || L <= 0) return r;
-  const long long F = see.frame, f = p / F;
+  const long long F = see.frame;
+  const long long f = see.frame == 1 ? p : static_cast<uint32_t>(p) / static_cast<uint32_t>(see.frame);
   long long end = L;  // keys a causal query may look at
   if (see.causal && (f + 1) * F < L) end = (f + 1) * F;
   long long s = see.sinks * F;

@@ -136,10 +136,17 @@ size_t carve_cache_attention(const sparsepr_cache_params& p,
   Carver w{base};
   w.at = carve_cache(p, base, &a->cache);
   if (q.Nq > 0) {
-    const CacheAttnPlan plan = cache_attn_plan(p, q.Hq, q.Nq);
+    const CacheAttnPlan plan = cache_attn_plan(p, q);
     a->pre = w.take<int32_t>(p.B + 1);
-    a->opart = w.take<float>(plan.slots * plan.rows * p.d);
-    a->lpart = w.take<float>(plan.slots * plan.rows);
+    a->opart = w.take<float>(plan.part_rows * p.d);
+    a->lpart = w.take<float>(plan.part_rows);
+    if (plan.wide) {
+      const size_t kv = static_cast<size_t>(plan.group) * p.Hkv * plan.cap * p.d;
+      a->kb = w.take<__nv_bfloat16>(kv);
+      a->vb = w.take<__nv_bfloat16>(kv);
+      // whatever the dtype of q: the size does not know it
+      a->qb = w.take<__nv_bfloat16>(static_cast<size_t>(plan.group) * q.Hq * q.Nq * p.d);
+    }
   }
   return w.at;
 }
@@ -201,7 +208,7 @@ sparsepr_status sparsepr_window_attention(const void* q, const void* k, const vo
   a.d = p->d;
   a.see = p->see;
   a.sc = log2_scale(p->scale, p->d);
-  a.bf16 = dt == SPARSEPR_BF16;
+  a.bf16 = a.kv_bf16 = dt == SPARSEPR_BF16;
   return cuda_status(launch_window_attention(a, static_cast<cudaStream_t>(stream)));
 }
 

@@ -27,6 +27,7 @@ constexpr int kDecodeThreads = kWarps * 32;
 constexpr int kMaxRows = 16;         // query rows of a block at most: 8 for each NT
 constexpr int kDecodeBlocks = 296;   // two per multiprocessor: one streams while the other merges
 constexpr int kMinTiles = kWarps;    // tiles per block at least (each goes to another warp)
+constexpr int kWideRows = 64;        // query rows per key head beyond which pages are widened
 constexpr int kDepth = 2;            // tiles of a warp: one in hand, one on its way
 
 // keys of a tile, at multiples of that in the sequence: 4 KB of keys and of values
@@ -129,7 +130,9 @@ struct PagedKV {
   int t0, t1;
   __device__ bool ok(int j) const {
     const int t = s.tile_of(j);
-    if (t < t0 || t >= t1) return false;
+    return t >= t0 && t < t1;
+  }
+  __device__ bool page_at(int j) const {
     const int id = row[j / a.p.page];
     return id >= 0 && id < a.p.n_pages;
   }
@@ -137,6 +140,7 @@ struct PagedKV {
     return static_cast<size_t>(row[j / a.p.page]) * a.p.Hkv + h;
   }
   __device__ float dot(int j, const float* q) const {
+    if (!page_at(j)) return __int_as_float(0x7fc00000);
     const uint8_t* k = static_cast<const uint8_t*>(a.c.k8) +
                        (slot(j) * a.p.page + j % a.p.page) * D;
     float s_ = 0.f;
@@ -144,6 +148,7 @@ struct PagedKV {
     return s_ * a.c.k_scale[slot(j)];
   }
   __device__ float v(int j, int c) const {
+    if (!page_at(j)) return __int_as_float(0x7fc00000);
     const uint8_t* x = static_cast<const uint8_t*>(a.c.v8) +
                        (slot(j) * a.p.page + j % a.p.page) * D;
     return from_e4m3(x[c]) * a.c.v_scale[slot(j)];
@@ -312,7 +317,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
   // ---- fetching: tile k of the warp is tile warp + 12 k of its run ----
   struct Look {  // one copy: page (-1: none to fetch), first key, scales
     int id, key0;
-    float ks, vs;
+    float ks, vs;  // ks < 0: no query sees these keys; NaN: the entry holds no page
   };
   struct Fetch {
     Run r;
@@ -334,6 +339,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
         if (x.id < 0 || x.id >= c.p.n_pages) {
           raise_status(c.stats, SPARSEPR_ERR_INVALID_ARG);
           x.id = -1;
+          x.ks = __int_as_float(0x7fc00000);  // logits of keys without a page are NaN
         }
       }
     }
@@ -545,7 +551,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
           const int from = (kth - f.batch) * spp + ((kt * 16) >> sub_shift);
           ks[kt] = __shfl_sync(0xffffffffu, from >= 0 ? f.now.ks : f.ks0, from & 31);
           lv[kt] = log2_of_scale(__shfl_sync(0xffffffffu, from >= 0 ? f.now.vs : f.vs0, from & 31));
-          whole = whole && !(ks[kt] < 0.f);
+          whole = whole && ks[kt] >= 0.f;
         }
         // one scale for all values of the tile: the two maxima differ by it
         bool one_scale = true;
@@ -634,7 +640,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
             if (!plain) {
               // a value that no row sees may be anything, also NaN
               const int kx = k0 + key;
-              if (ks[kt] < 0.f || !(kx < s.SA || (kx >= s.LB && kx < s.HB)))
+              if (!(ks[kt] >= 0.f) || !(kx < s.SA || (kx >= s.LB && kx < s.HB)))
 #pragma unroll
                 for (int w = 0; w < kW; ++w) vw[e][w] = 0u;
             }
@@ -878,6 +884,48 @@ __global__ void __launch_bounds__(NT* 256) cache_combine_kernel(const DecodePara
   if (a.lse && lane == 0) a.lse[row] = lse * kLn2F;
 }
 
+// Many query rows: the tokens that some query sees, widened to bf16 rows
+// [sequence - b0, head, position, HD] (exact: 4 significant bits times a power of
+// two). One block per tile of a sequence and head.
+template <int HD>
+__global__ void __launch_bounds__(256)
+    widen_kernel(const CacheAttnArgs a, int b0, int cap, __nv_bfloat16* kb, __nv_bfloat16* vb) {
+  const CacheArgs& c = a.cache;
+  const int h = blockIdx.y, b = b0 + blockIdx.z;
+  const SeqTiles s = seq_tiles(a, b, false);
+  if (static_cast<int>(blockIdx.x) >= s.T) return;
+  constexpr int kPieces = 4096 / 16;  // 16-byte pieces of the tile's keys, one per thread
+  static_assert(kPieces == 256, "threads");
+  const int key = s.start(blockIdx.x) + threadIdx.x * 16 / HD, col = threadIdx.x * 16 % HD;
+  if (key >= s.L) return;
+  const int id = c.c.table[static_cast<size_t>(b) * c.p.max_pages + key / c.p.page];
+  const size_t to = ((static_cast<size_t>(blockIdx.z) * c.p.Hkv + h) * cap + key) * HD + col;
+  const bool page = id >= 0 && id < c.p.n_pages;
+  if (!page && (key < s.SA || (key >= s.LB && key < s.HB)))
+    raise_status(c.stats, SPARSEPR_ERR_INVALID_ARG);
+  const size_t slot = static_cast<size_t>(page ? id : 0) * c.p.Hkv + h;
+  const size_t from = (slot * c.p.page + key % c.p.page) * HD + col;
+#pragma unroll
+  for (int kv = 0; kv < 2; ++kv) {
+    uint4 u[2];
+    if (page) {
+      const float scale = (kv ? c.c.v_scale : c.c.k_scale)[slot];
+      float x[16];
+      from_e4m3_16(*reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(kv ? c.c.v8 : c.c.k8) + from), x);
+      uint32_t w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(x[2 * i] * scale, x[2 * i + 1] * scale);
+      u[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      u[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    } else {  // NaN: a query that needs the token shows it
+      u[0] = u[1] = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+    }
+    uint4* dst = reinterpret_cast<uint4*>((kv ? vb : kb) + to);
+    dst[0] = u[0];
+    dst[1] = u[1];
+  }
+}
+
 // [n_pages, Hkv * page, HD] bytes, swizzled over the whole row
 bool make_page_map(CUtensorMap* m, const void* base, const sparsepr_cache_params& p, int box_rows) {
   EncodeTiledFn enc = encode_tiled_fn();
@@ -923,18 +971,80 @@ cudaError_t launch_decode_rows(const DecodeParams& p, const DecodeMaps& maps, cu
 
 }  // namespace
 
-CacheAttnPlan cache_attn_plan(const sparsepr_cache_params& p, int Hq, int Nq) {
+CacheAttnPlan cache_attn_plan(const sparsepr_cache_params& p, const sparsepr_cache_attention_params& q) {
   CacheAttnPlan w = {};
-  const int R = Hq / p.Hkv * Nq;
+  const long long R = static_cast<long long>(q.Hq / p.Hkv) * q.Nq;
+  w.wide = R > kWideRows;
+  if (w.wide) {
+    // bf16 rows of as many sequences at a time as fit 1 GB
+    w.cap = p.max_pages * p.page;
+    const long long bytes = 4ll * p.Hkv * w.cap * p.d;
+    long long g = (1ll << 30) / bytes;
+    w.group = static_cast<int>(g < 1 ? 1 : g < p.B ? g : p.B);
+    for (int n : {w.group, p.B % w.group}) {
+      if (n == 0) continue;
+      const WindowPlan plan = window_plan(n, q.Hq, p.Hkv, q.Nq, w.cap, q.see);
+      const size_t rows = plan.splits > 1
+                              ? static_cast<size_t>(plan.units) * plan.splits * plan.unit_rows : 0;
+      if (rows > w.part_rows) w.part_rows = rows;
+    }
+    return w;
+  }
   w.rows = R <= 8 ? 8 : 16;
-  w.row_tiles = (R + w.rows - 1) / w.rows;
-  w.slots = static_cast<size_t>(p.B) * p.Hkv * w.row_tiles + kDecodeBlocks;
+  w.row_tiles = static_cast<int>((R + w.rows - 1) / w.rows);
+  w.part_rows = (static_cast<size_t>(p.B) * p.Hkv * w.row_tiles + kDecodeBlocks) * w.rows;
   return w;
 }
 
+namespace {
+
+cudaError_t launch_wide(const CacheAttnArgs& a, const CacheAttnPlan& w, cudaStream_t st) {
+  const sparsepr_cache_params& p = a.cache.p;
+  WindowArgs x = {};
+  x.Hq = a.Hq;
+  x.Hkv = p.Hkv;
+  x.Nq = a.Nq;
+  x.Nk = w.cap;
+  x.d = p.d;
+  x.see = a.see;
+  x.sc = a.sc;
+  x.bf16 = a.bf16;
+  x.kv_bf16 = true;
+  x.k = a.kb;
+  x.v = a.vb;
+  x.stats = a.cache.stats;
+  x.qb = a.qb;
+  x.opart = a.opart;
+  x.lpart = a.lpart;
+  const size_t row = static_cast<size_t>(p.d) * (a.bf16 ? 2 : 4);
+  for (int b0 = 0; b0 < p.B; b0 += w.group) {
+    const size_t q0 = static_cast<size_t>(b0) * a.Hq * a.Nq;
+    x.B = min(w.group, p.B - b0);
+    const dim3 grid((w.cap + tile_keys(p.d) - 1) / tile_keys(p.d), p.Hkv, x.B);
+    if (p.d == 128) widen_kernel<128><<<grid, 256, 0, st>>>(a, b0, w.cap, a.kb, a.vb);
+    else widen_kernel<64><<<grid, 256, 0, st>>>(a, b0, w.cap, a.kb, a.vb);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    x.q = static_cast<const char*>(a.q) + q0 * row;
+    x.out = static_cast<char*>(a.out) + q0 * row;
+    x.lse = a.lse ? a.lse + q0 : nullptr;
+    x.n_q = a.n_q ? a.n_q + b0 : nullptr;
+    x.n_k = a.cache.c.len + b0;
+    if ((e = launch_window_attention(x, st)) != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace
+
 cudaError_t launch_cache_attention(const CacheAttnArgs& a, cudaStream_t st) {
   if (a.Nq == 0) return cudaSuccess;
-  const CacheAttnPlan w = cache_attn_plan(a.cache.p, a.Hq, a.Nq);
+  sparsepr_cache_attention_params q = {};
+  q.Hq = a.Hq;
+  q.Nq = a.Nq;
+  q.see = a.see;
+  const CacheAttnPlan w = cache_attn_plan(a.cache.p, q);
+  if (w.wide) return launch_wide(a, w, st);
   DecodeParams p = {};
   p.a = a;
   p.group = a.Hq / a.cache.p.Hkv;

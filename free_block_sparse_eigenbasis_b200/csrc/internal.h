@@ -313,6 +313,7 @@ struct WindowArgs {
   sparsepr_visibility see;
   float sc;  // scale * log2(e)
   bool bf16;
+  bool kv_bf16;  // k and v are bf16 whatever the dtype of q and out
   DeviceStats* stats;
   // scratch in the workspace
   __nv_bfloat16 *qb, *kb, *vb;  // fp32 inputs rounded to bf16
@@ -366,13 +367,17 @@ struct CacheAttnArgs {
   // scratch in the workspace
   int32_t* pre;          // [B + 1] tiles before each sequence
   float *opart, *lpart;  // partial outputs and log2-sum-exps of units cut over blocks
+  __nv_bfloat16 *qb, *kb, *vb;  // fp32 queries rounded to bf16, widened pages
 };
 struct CacheAttnPlan {
-  int rows;       // query rows of a unit
-  int row_tiles;  // units per key head
-  size_t slots;   // partial results of `rows` rows
+  bool wide;         // pages are widened and read by the windowed attention
+  int rows;          // query rows of a unit (not wide)
+  int row_tiles;     // units per key head
+  int cap, group;    // rows per sequence and sequences at a time of the widened pages
+  size_t part_rows;  // rows of partial results
 };
-CacheAttnPlan cache_attn_plan(const sparsepr_cache_params& p, int Hq, int Nq);
+CacheAttnPlan cache_attn_plan(const sparsepr_cache_params& p,
+                              const sparsepr_cache_attention_params& q);
 cudaError_t launch_cache_attention(const CacheAttnArgs& a, cudaStream_t st);
 
 cudaError_t launch_pairs_exec(const int64_t* pairs_sparse, int H, int64_t add, int64_t* pairs_exec,

@@ -52,7 +52,7 @@ struct Bars {
   uint64_t q_full;
   uint64_t kfull[kStages], vfull[kStages], kempty[kStages], vempty[kStages];
   uint64_t vfix[2];
-  uint64_t s_full[2], p_full[2], o_done[2];
+  uint64_t s_full[2], p_full[2][2], pa_done[2], o_done[2];
   uint64_t mma_idle;
   uint32_t tmem_base;
   int abort;
@@ -101,6 +101,13 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
       " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
       : "memory");
+}
+
+// one lane of the (converged) warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t is;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(is));
+  return is != 0;
 }
 
 // bits [a, b) of a 32-bit word (any a, b)
@@ -279,7 +286,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->vfix[i], 1);
       mbar_init(&bars->s_full[i], 1);
-      mbar_init(&bars->p_full[i], kTileM);
+      mbar_init(&bars->p_full[i][0], kTileM);
+      mbar_init(&bars->p_full[i][1], kTileM);
+      mbar_init(&bars->pa_done[i], 1);
       mbar_init(&bars->o_done[i], 1);
     }
     mbar_init(&bars->mma_idle, 1);
@@ -348,67 +357,88 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 9) {
     // ------------------------------ MMA issuer --------------------------------
-    if (lane == 0) {
-      constexpr uint32_t idS = idesc_bf16(kTileM, kTileN, 0);
-      constexpr uint32_t idO = idesc_bf16(kTileM, HD, 1);
-      const uint32_t q_addr = smem_u32(Qs), k_addr = smem_u32(Ks), v_addr = smem_u32(Vs);
-      bool ok = mbar_wait(&bars->q_full, 0, abort);
-      auto kv_of = [&](int i, int t) { return two ? t : 2 * t + i; };
-      // S_i = Q_(tile of i) K(kv)^T
-      auto issue_s = [&](int i, int t) -> bool {
-        const int kv = kv_of(i, t), st = kv % kStages;
-        if (!mbar_wait(&bars->kfull[st], (kv / kStages) & 1, abort)) return false;
-        tc_fence_after();
-        const uint32_t qa = q_addr + (two ? i : 0) * L::kTileBytes;
-        const uint32_t d_tmem = tmem + static_cast<uint32_t>(i * kTileN);
+    // The whole warp walks the loop, so that addresses stay in uniform registers,
+    // and one elected lane issues; a descriptor is a base plus a constant (with
+    // one lane in the loop, each product took 120 cycles to issue, not 64).
+    constexpr uint32_t idS = idesc_bf16(kTileM, kTileN, 0);
+    constexpr uint32_t idO = idesc_bf16(kTileM, HD, 1);
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint64_t q_desc = smem_desc_sw128(smem_u32(Qs), 16, 1024);
+    const uint64_t k_desc = smem_desc_sw128(smem_u32(Ks), 16, 1024);
+    const uint64_t v_desc = smem_desc_sw128(smem_u32(Vs), L::kSlab, 1024);
+    const bool leader = elect_one();
+    bool ok = __all_sync(0xffffffffu, mbar_wait(&bars->q_full, 0, abort));
+    auto kv_of = [&](int i, int t) { return two ? t : 2 * t + i; };
+    // S_i = Q_(tile of i) K(kv)^T
+    auto issue_s = [&](int i, int t) -> bool {
+      const int kv = kv_of(i, t), st = kv % kStages;
+      if (!__all_sync(0xffffffffu, mbar_wait(&bars->kfull[st], (kv / kStages) & 1, abort))) return false;
+      tc_fence_after();
+      const uint64_t qd = q_desc + static_cast<uint64_t>((two ? i : 0) * (L::kTileBytes >> 4));
+      const uint64_t kd = k_desc + static_cast<uint64_t>(st * (L::kTileBytes >> 4));
+      const uint32_t d_tmem = tm + static_cast<uint32_t>(i * kTileN);
+      if (leader) {
 #pragma unroll
         for (int ks = 0; ks < HD / 16; ++ks) {
-          const uint32_t off = static_cast<uint32_t>((ks >> 2) * L::kSlab + (ks & 3) * 32);
-          mma_bf16_ss(d_tmem, smem_desc_sw128(qa + off, 16, 1024),
-                      smem_desc_sw128(k_addr + st * L::kTileBytes + off, 16, 1024), idS,
-                      ks > 0 ? 1u : 0u);
+          const uint64_t off = ((ks >> 2) * L::kSlab + (ks & 3) * 32) >> 4;
+          mma_bf16_ss(d_tmem, qd + off, kd + off, idS, ks > 0 ? 1u : 0u);
         }
         mma_commit(&bars->s_full[i]);
         if (!two || i == 1) mma_commit(&bars->kempty[st]);  // last reader of K(kv)
-        return true;
-      };
-      // O_i += P_i V(kv), P_i from tensor memory
-      int fixes = 0, fix_of = -1;
-      auto issue_pv = [&](int i, int t) -> bool {
-        const int kv = kv_of(i, t), st = kv % kStages;
-        if (!mbar_wait(&bars->p_full[i], t & 1, abort)) return false;
-        if (!mbar_wait(&bars->vfull[st], (kv / kStages) & 1, abort)) return false;
-        if (kv != fix_of && needs_fix(j0 + kv)) {
-          if (!mbar_wait(&bars->vfix[fixes], 0, abort)) return false;
-          fix_of = kv;
-          ++fixes;
-        }
-        tc_fence_after();
-        const uint32_t o_tmem = tmem + 2u * kTileN + static_cast<uint32_t>(i * HD);
-        const uint32_t p_tmem = tmem + static_cast<uint32_t>(i * kTileN);
+      }
+      __syncwarp();
+      return true;
+    };
+    // O_i += P_i V(kv), P_i from tensor memory, each half as soon as it is stored
+    int fixes = 0, fix_of = -1;
+    auto issue_pv = [&](int i, int t) -> bool {
+      const int kv = kv_of(i, t), st = kv % kStages;
+      if (!__all_sync(0xffffffffu, mbar_wait(&bars->vfull[st], (kv / kStages) & 1, abort))) return false;
+      if (kv > fix_of && needs_fix(j0 + kv)) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&bars->vfix[fixes], 0, abort))) return false;
+        fix_of = kv;
+        ++fixes;
+      }
+      const uint64_t vd = v_desc + static_cast<uint64_t>(st * (L::kTileBytes >> 4));
+      const uint32_t o_tmem = tm + 2u * kTileN + static_cast<uint32_t>(i * HD);
+      const uint32_t p_tmem = tm + static_cast<uint32_t>(i * kTileN);
 #pragma unroll
-        for (int ks = 0; ks < kTileN / 16; ++ks)
-          mma_bf16_ts(o_tmem, p_tmem + static_cast<uint32_t>(ks * 8),
-                      smem_desc_sw128(v_addr + st * L::kTileBytes + ks * 16 * 128, L::kSlab, 1024),
-                      idO, (t > 0 || ks > 0) ? 1u : 0u);
-        if (!two || i == 1) mma_commit(&bars->vempty[st]);  // last reader of V(kv)
-        if (t == ntask[i] - 1) mma_commit(&bars->o_done[i]);
-        return true;
-      };
-      for (int i = 0; i < 2 && ok; ++i)
-        if (ntask[i] > 0) ok = issue_s(i, 0);
-      const int nt = max(ntask[0], ntask[1]);
-      for (int t = 0; t < nt && ok; ++t)
-        for (int i = 0; i < 2 && ok; ++i) {
-          if (t >= ntask[i]) continue;
-          ok = issue_pv(i, t);
-          if (ok && t + 1 < ntask[i]) ok = issue_s(i, t + 1);
+      for (int hf = 0; hf < 2; ++hf) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&bars->p_full[i][hf], t & 1, abort))) return false;
+        tc_fence_after();
+        if (leader) {
+#pragma unroll
+          for (int k = 0; k < kTileN / 32; ++k) {
+            const int ks = hf * (kTileN / 32) + k;
+            mma_bf16_ts(o_tmem, p_tmem + static_cast<uint32_t>(ks * 8),
+                        vd + static_cast<uint64_t>((ks * 16 * 128) >> 4), idO,
+                        (t > 0 || ks > 0) ? 1u : 0u);
+          }
+          if (hf == 0) {
+            mma_commit(&bars->pa_done[i]);
+          } else {
+            if (!two || i == 1) mma_commit(&bars->vempty[st]);  // last reader of V(kv)
+            if (t == ntask[i] - 1) mma_commit(&bars->o_done[i]);
+          }
         }
-      // all issued MMAs complete before the block releases tensor memory
-      mma_commit(&bars->mma_idle);
-      volatile int never = 0;
-      mbar_wait(&bars->mma_idle, 0, &never);
-    }
+        __syncwarp();
+      }
+      return true;
+    };
+    for (int i = 0; i < 2 && ok; ++i)
+      if (ntask[i] > 0) ok = issue_s(i, 0);
+    const int nt = max(ntask[0], ntask[1]);
+    for (int t = 0; t < nt && ok; ++t)
+      for (int i = 0; i < 2 && ok; ++i) {
+        if (t >= ntask[i]) continue;
+        ok = issue_pv(i, t);
+        if (ok && t + 1 < ntask[i]) ok = issue_s(i, t + 1);
+      }
+    // all issued MMAs complete before the block releases tensor memory
+    if (leader) mma_commit(&bars->mma_idle);
+    __syncwarp();
+    volatile int never = 0;
+    mbar_wait(&bars->mma_idle, 0, &never);
   } else {
     // ------------- softmax: warpgroup i = warp / 4, thread = row -------------
     const int i = warp >> 2;
@@ -491,9 +521,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // later tiles are exponentiated against it with no
       // maximum pass. A half whose sum exceeds 2^32 moves the reference up by
       // the whole number k of log2 units that brings its largest value to at
-      // most 1: its values are formed again, and the P half already stored,
-      // the row sum and O are scaled by 2^-k, exactly. O and the row sum
-      // always share one reference, so the result is exact.
+      // most 1: its values are formed again, and the row sum and O are scaled
+      // by 2^-k, exactly. O and the row sum always share one reference, so the
+      // result is exact.
       if (__any_sync(0xffffffffu, m_ref == -INFINITY)) {
         load_half(0);
         const float m0 = half_max();
@@ -501,8 +531,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float mt = fmaxf(m0, half_max());
         if (m_ref == -INFINITY) m_ref = ceilf(mt);
       }
-      float alpha = 1.f, rs = 0.f;
-      bool need = false;
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
         load_half(hf);
@@ -515,44 +543,35 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float k = fminf(ceilf(half_max() - m_ref), 16384.f);
             sh = (k < 127.f) ? __int_as_float((127 - static_cast<int>(k)) << 23) : 0.f;
             m_ref += k;
-            need = true;
-          }
-          alpha *= sh;
-          rs *= sh;
-          if (hf == 1 && __any_sync(0xffffffffu, sh != 1.f)) {
-            // the stored P half 0 follows the new reference (exact: a power of two)
-            uint32_t q[32];
-            tmem_ld32(s_tmem, q);
-            tmem_wait_ld();
-#pragma unroll
-            for (int c = 0; c < 32; ++c)
-              q[c] = pack_bf16x2(__uint_as_float(q[c] << 16) * sh,
-                                 __uint_as_float(q[c] & 0xFFFF0000u) * sh);
-            tmem_st32(s_tmem, q);
           }
           rh = exp_half(m_ref);
+          l_sum *= sh;
+          // O holds the products of the tiles before (they precede S_i(t)) and, in
+          // the second half, those of the first half
+          bool there = true;
+          if (hf == 1) there = mbar_wait(&bars->pa_done[i], t & 1, abort);
+          if (!__all_sync(0xffffffffu, there)) { ok = false; break; }
+          tc_fence_after();
+          if (t > 0 || hf == 1) {
+            const uint32_t o_tmem = o_base + static_cast<uint32_t>(i * HD);
+#pragma unroll 1
+            for (int c = 0; c < HD / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(o_tmem + c * 32, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * sh);
+              tmem_st32(o_tmem + c * 32, o);
+            }
+          }
         }
         tmem_st32(s_tmem + hf * 32, pk);
-        rs += rh;
+        l_sum += rh;
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&bars->p_full[i][hf]);
       }
-      if (__any_sync(0xffffffffu, need)) {
-        // P_i(t-1) V has completed (it precedes S_i(t)); O_i is not read again
-        // before P_i(t) is published below
-        const uint32_t o_tmem = o_base + static_cast<uint32_t>(i * HD);
-#pragma unroll 1
-        for (int c = 0; c < HD / 32; ++c) {
-          uint32_t o[32];
-          tmem_ld32(o_tmem + c * 32, o);
-          tmem_wait_ld();
-#pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-          tmem_st32(o_tmem + c * 32, o);
-        }
-      }
-      l_sum = l_sum * alpha + rs;
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(&bars->p_full[i]);
+      if (!ok) break;
     }
     // ---------------- epilogue: O / l -> global -------------------------------
     float f0, f1 = 0.f, lsev;  // factors of this thread's O and the other one's, log2-sum-exp
@@ -827,7 +846,7 @@ cudaError_t launch_window_attention(const WindowArgs& in, cudaStream_t st) {
     if ((e = launch_cast_bf16(static_cast<const float*>(a.q), a.qb, q_rows * a.d, st)) != cudaSuccess)
       return e;
     a.q = a.qb;
-    if (kv_rows > 0) {
+    if (kv_rows > 0 && !a.kv_bf16) {
       if ((e = launch_cast_bf16(static_cast<const float*>(a.k), a.kb, kv_rows * a.d, st)) != cudaSuccess ||
           (e = launch_cast_bf16(static_cast<const float*>(a.v), a.vb, kv_rows * a.d, st)) != cudaSuccess)
         return e;

@@ -413,26 +413,23 @@ F8 = torch.float8_e4m3fn
 
 
 def _visibility(p: dict) -> Visibility:
-    return Visibility(int(p.get("frame", 1)), int(p.get("window", 0)), int(p.get("sinks", 0)),
-                      int(p.get("causal", 1)))
+    return Visibility(p.get("frame", 1), p.get("window", 0), p.get("sinks", 0), p.get("causal", 1))
 
 
 def make_window_params(p: dict) -> WindowParams:
     """ctypes parameters of the windowed attention from a plain dict (B, Hq,
     Hkv, Nq, Nk, d; frame, window, sinks, causal as in sparsepr_visibility,
     by default token-causal without a window; scale)."""
-    return WindowParams(int(p["B"]), int(p["Hq"]), int(p["Hkv"]), int(p["Nq"]), int(p["Nk"]),
-                        int(p["d"]), _visibility(p), float(p.get("scale", 0.0)))
+    return WindowParams(p["B"], p["Hq"], p["Hkv"], p["Nq"], p["Nk"], p["d"], _visibility(p),
+                        p.get("scale", 0.0))
 
 
 def make_cache_params(p: dict) -> CacheParams:
-    return CacheParams(int(p["B"]), int(p["Hkv"]), int(p["d"]), int(p["page"]), int(p["n_pages"]),
-                       int(p["max_pages"]))
+    return CacheParams(p["B"], p["Hkv"], p["d"], p["page"], p["n_pages"], p["max_pages"])
 
 
 def make_cache_attention_params(a: dict) -> CacheAttentionParams:
-    return CacheAttentionParams(int(a["Hq"]), int(a["Nq"]), _visibility(a),
-                                float(a.get("scale", 0.0)))
+    return CacheAttentionParams(a["Hq"], a["Nq"], _visibility(a), a.get("scale", 0.0))
 
 
 @dataclass
@@ -488,23 +485,38 @@ def allocate_cache_workspace(p: dict, attn: Optional[dict] = None, device="cuda"
 _DTYPE_CODES = {torch.bfloat16: BF16, torch.float32: F32}
 
 
-def _opt(t, name, shape, dtype):
-    return None if t is None else _arg(t, name, shape, dtype)
+def _ptr(t, name, shape, dtype, dev):
+    """Device pointer (int) of a tensor argument on device index dev: the checks
+    of _arg in one expression, _arg itself for the message when one fails."""
+    if (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype
+            and t.is_contiguous() and t.get_device() == dev
+            and (dev >= 0 or _DEVICE_TYPE == "cpu")):
+        return t.data_ptr()
+    _arg(t, name, shape, dtype)
+    raise ValueError("%s must be on the device of the workspace" % name)
 
 
-def _call(where: str, fn, tensors, args, ws, stream):
+def _launch(where: str, fn, args, ws, dev, stream):
     """One library call on the device of its tensors and, unless a stream is
     given, on that device's current stream."""
-    wp, wb = _ws(ws)
-    dev = ws.device
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError("%s: all tensors must be on one device" % where)
-    if dev.type != "cuda" or dev.index == torch.cuda.current_device():
-        _check(fn(*args, wp, wb, _stream(stream)), where)
-        return
-    with torch.cuda.device(dev):
-        _check(fn(*args, wp, wb, _stream(stream)), where)
+    if not (ws.dtype is torch.uint8 and ws.is_contiguous() and (dev >= 0 or _DEVICE_TYPE == "cpu")):
+        _ws(ws)
+    wp, wb = ws.data_ptr(), ws.numel()
+    if dev < 0 or dev == torch.cuda.current_device():
+        st = (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+        code = fn(*args, wp, wb, st)
+    else:
+        with torch.cuda.device(dev):
+            st = (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+            code = fn(*args, wp, wb, st)
+    if code != OK:
+        raise SparsePRError(code, where)
+
+
+def _device(ws) -> int:
+    if not isinstance(ws, torch.Tensor):
+        raise TypeError("ws must be a torch.Tensor")
+    return ws.get_device()
 
 
 def sparsepr_window_attention(q, k, v, p: dict, out, ws, lse=None, n_q=None, n_k=None,
@@ -513,94 +525,100 @@ def sparsepr_window_attention(q, k, v, p: dict, out, ws, lse=None, n_q=None, n_k
     [B, Hq, Nq, d], k, v [B, Hkv, Nk, d] bf16 or fp32; lse [B, Hq, Nq] fp32,
     n_q and n_k [B] int32, each optional (see include/sparsepr.h)."""
     prm = make_window_params(p)
-    B, Hq, Hkv, Nq, Nk, d = prm.B, prm.Hq, prm.Hkv, prm.Nq, prm.Nk, prm.d
+    B, Hq, Nq, d, dev, t = prm.B, prm.Hq, prm.Nq, prm.d, _device(ws), q.dtype
     dt = _dtype_code(q)
-    _call("sparsepr_window_attention", lib.sparsepr_window_attention,
-          (q, k, v, out, lse, n_q, n_k),
-          (_arg(q, "q", (B, Hq, Nq, d)), _arg(k, "k", (B, Hkv, Nk, d), q.dtype),
-           _arg(v, "v", (B, Hkv, Nk, d), q.dtype), dt, ctypes.byref(prm),
-           _opt(n_q, "n_q", (B,), I32), _opt(n_k, "n_k", (B,), I32),
-           _arg(out, "out", (B, Hq, Nq, d), q.dtype),
-           _opt(lse, "lse", (B, Hq, Nq), torch.float32)), ws, stream)
+    rows, keys = (B, Hq, Nq, d), (B, prm.Hkv, prm.Nk, d)
+    _launch("sparsepr_window_attention", lib.sparsepr_window_attention,
+            (_ptr(q, "q", rows, t, dev), _ptr(k, "k", keys, t, dev), _ptr(v, "v", keys, t, dev),
+             dt, ctypes.byref(prm), None if n_q is None else _ptr(n_q, "n_q", (B,), I32, dev),
+             None if n_k is None else _ptr(n_k, "n_k", (B,), I32, dev),
+             _ptr(out, "out", rows, t, dev),
+             None if lse is None else _ptr(lse, "lse", (B, Hq, Nq), torch.float32, dev)),
+            ws, dev, stream)
 
 
-def _cache(p: dict, c: Cache):
-    prm = make_cache_params(p)
+def _cache(p: dict, c: Cache, ws):
+    """(parameters, their reference, reference to the pointers, device)"""
+    prm, dev = make_cache_params(p), _device(ws)
     pages, f32 = (prm.n_pages, prm.Hkv), torch.float32
+    pool = pages + (prm.page, prm.d)
     ptr = CachePointers(
-        _arg(c.k8, "k8", pages + (prm.page, prm.d), F8), _arg(c.v8, "v8", pages + (prm.page, prm.d), F8),
-        _arg(c.k_scale, "k_scale", pages, f32), _arg(c.v_scale, "v_scale", pages, f32),
-        _arg(c.table, "table", (prm.B, prm.max_pages), I32), _arg(c.len, "len", (prm.B,), I32),
-        _arg(c.ref, "ref", (prm.n_pages,), I32))
-    return prm, ctypes.byref(prm), ctypes.byref(ptr), (c.k8, c.v8, c.k_scale, c.v_scale, c.table,
-                                                       c.len, c.ref)
+        _ptr(c.k8, "k8", pool, F8, dev), _ptr(c.v8, "v8", pool, F8, dev),
+        _ptr(c.k_scale, "k_scale", pages, f32, dev), _ptr(c.v_scale, "v_scale", pages, f32, dev),
+        _ptr(c.table, "table", (prm.B, prm.max_pages), I32, dev),
+        _ptr(c.len, "len", (prm.B,), I32, dev), _ptr(c.ref, "ref", (prm.n_pages,), I32, dev))
+    return prm, ctypes.byref(prm), ctypes.byref(ptr), dev
 
 
 def sparsepr_cache_reserve(n_new, p: dict, cache: Cache, start, ws, stream=None):
     """Pages for n_new [B] int32 more tokens per sequence; start [B] int32
     receives the lengths before (-1 throughout if there is no room)."""
-    prm, pp, cp, ts = _cache(p, cache)
-    _call("sparsepr_cache_reserve", lib.sparsepr_cache_reserve, ts + (n_new, start),
-          (pp, cp, _arg(n_new, "n_new", (prm.B,), I32), _arg(start, "start", (prm.B,), I32)), ws,
-          stream)
+    prm, pp, cp, dev = _cache(p, cache, ws)
+    _launch("sparsepr_cache_reserve", lib.sparsepr_cache_reserve,
+            (pp, cp, _ptr(n_new, "n_new", (prm.B,), I32, dev),
+             _ptr(start, "start", (prm.B,), I32, dev)), ws, dev, stream)
 
 
 def sparsepr_cache_append(k, v, p: dict, cache: Cache, start, n_new, ws, stream=None):
     """Write the tokens k, v [B, Hkv, T, d] (bf16 or fp32; the first n_new[b]
     of each sequence, all T where n_new is None) at start[b] in 8 bits."""
-    prm, pp, cp, ts = _cache(p, cache)
+    prm, pp, cp, dev = _cache(p, cache, ws)
     dt = _dtype_code(k)
     shape = (prm.B, prm.Hkv, k.shape[2] if k.dim() == 4 else -1, prm.d)
-    _call("sparsepr_cache_append", lib.sparsepr_cache_append, ts + (k, v, start, n_new),
-          (_arg(k, "k", shape), _arg(v, "v", shape, k.dtype), dt, shape[2], pp, cp,
-           _arg(start, "start", (prm.B,), I32), _opt(n_new, "n_new", (prm.B,), I32)), ws, stream)
+    _launch("sparsepr_cache_append", lib.sparsepr_cache_append,
+            (_ptr(k, "k", shape, k.dtype, dev), _ptr(v, "v", shape, k.dtype, dev), dt, shape[2],
+             pp, cp, _ptr(start, "start", (prm.B,), I32, dev),
+             None if n_new is None else _ptr(n_new, "n_new", (prm.B,), I32, dev)), ws, dev, stream)
 
 
 def sparsepr_cache_attention(q, p: dict, cache: Cache, attn: dict, out, ws, lse=None, n_q=None,
                              stream=None):
     """Attention of q [B, Hq, Nq, d] over the cached tokens; attn: Hq, Nq and
     the visibility (see include/sparsepr.h)."""
-    prm, pp, cp, ts = _cache(p, cache)
+    prm, pp, cp, dev = _cache(p, cache, ws)
     a = make_cache_attention_params(attn)
-    shape = (prm.B, a.Hq, a.Nq, prm.d)
+    rows = (prm.B, a.Hq, a.Nq, prm.d)
     dt = _dtype_code(q)
-    _call("sparsepr_cache_attention", lib.sparsepr_cache_attention, ts + (q, out, lse, n_q),
-          (_arg(q, "q", shape), dt, pp, cp, ctypes.byref(a), _opt(n_q, "n_q", (prm.B,), I32),
-           _arg(out, "out", shape, q.dtype), _opt(lse, "lse", shape[:3], torch.float32)), ws,
-          stream)
+    _launch("sparsepr_cache_attention", lib.sparsepr_cache_attention,
+            (_ptr(q, "q", rows, q.dtype, dev), dt, pp, cp, ctypes.byref(a),
+             None if n_q is None else _ptr(n_q, "n_q", (prm.B,), I32, dev),
+             _ptr(out, "out", rows, q.dtype, dev),
+             None if lse is None else _ptr(lse, "lse", rows[:3], torch.float32, dev)), ws, dev,
+            stream)
 
 
 def sparsepr_cache_fork(src, dst, p: dict, cache: Cache, ws, stream=None):
     """Sequence dst[i] becomes a copy of sequence src[i] that shares its pages."""
-    prm, pp, cp, ts = _cache(p, cache)
+    _, pp, cp, dev = _cache(p, cache, ws)
     n = src.numel()
-    _call("sparsepr_cache_fork", lib.sparsepr_cache_fork, ts + (src, dst),
-          (pp, cp, _arg(src, "src", (n,), I32), _arg(dst, "dst", (n,), I32), n), ws, stream)
+    _launch("sparsepr_cache_fork", lib.sparsepr_cache_fork,
+            (pp, cp, _ptr(src, "src", (n,), I32, dev), _ptr(dst, "dst", (n,), I32, dev), n), ws,
+            dev, stream)
 
 
 def sparsepr_cache_free(seq, p: dict, cache: Cache, ws, stream=None):
     """Empty the sequences named in seq [n] int32."""
-    prm, pp, cp, ts = _cache(p, cache)
+    _, pp, cp, dev = _cache(p, cache, ws)
     n = seq.numel()
-    _call("sparsepr_cache_free", lib.sparsepr_cache_free, ts + (seq,),
-          (pp, cp, _arg(seq, "seq", (n,), I32), n), ws, stream)
+    _launch("sparsepr_cache_free", lib.sparsepr_cache_free,
+            (pp, cp, _ptr(seq, "seq", (n,), I32, dev), n), ws, dev, stream)
 
 
 def sparsepr_cache_evict(see: dict, p: dict, cache: Cache, ws, stream=None):
     """Give up the pages that no later query with this causal, windowed
     visibility can see."""
-    prm, pp, cp, ts = _cache(p, cache)
+    _, pp, cp, dev = _cache(p, cache, ws)
     v = _visibility(see)
-    _call("sparsepr_cache_evict", lib.sparsepr_cache_evict, ts, (pp, cp, ctypes.byref(v)), ws,
-          stream)
+    _launch("sparsepr_cache_evict", lib.sparsepr_cache_evict, (pp, cp, ctypes.byref(v)), ws, dev,
+            stream)
 
 
 def sparsepr_cache_compact(p: dict, cache: Cache, n_used, ws, stream=None):
     """Move the pages in use to the front of the pool; n_used [1] int32
     receives their number."""
-    prm, pp, cp, ts = _cache(p, cache)
-    _call("sparsepr_cache_compact", lib.sparsepr_cache_compact, ts + (n_used,),
-          (pp, cp, _arg(n_used, "n_used", (1,), I32)), ws, stream)
+    _, pp, cp, dev = _cache(p, cache, ws)
+    _launch("sparsepr_cache_compact", lib.sparsepr_cache_compact,
+            (pp, cp, _ptr(n_used, "n_used", (1,), I32, dev)), ws, dev, stream)
 
 
 _REGION_DTYPES = dict(init_k=torch.int32, init_q=torch.int32, zplanes=torch.bfloat16,

@@ -531,10 +531,13 @@ sparsepr_status sparsepr_cache_append(const void* k, const void* v, sparsepr_dty
 /* Attention over the cache: sparsepr_window_attention with the keys and
  * values that the pages of each sequence stand for, L = len[b].
  *   q [B, Hq, Nq, d] dtype dt, n_q, out, lse as there.
- * Queries are rounded to 11 significant bits at least, weights likewise, the
- * softmax and its sums are fp32. A visible token whose table entry holds no
- * page counts as not visible and raises SPARSEPR_ERR_INVALID_ARG, as do n_q
- * outside [0, Nq] and len outside the table (clamped). */
+ * Up to 64 query rows per key head (Hq / Hkv * Nq) the cache is read in place,
+ * queries and weights are rounded to 11 significant bits; beyond that the pages
+ * are widened to bf16 in ws first and queries and weights are rounded to bf16 (8
+ * bits), as in sparsepr_window_attention. The softmax and all sums are fp32.
+ * A token whose table entry holds no page raises SPARSEPR_ERR_INVALID_ARG and
+ * makes the rows that see it NaN; n_q outside [0, Nq] and len outside the
+ * table raise it too and are clamped. */
 sparsepr_status sparsepr_cache_attention(const void* q, sparsepr_dtype dt,
                                          const sparsepr_cache_params* p, const sparsepr_cache* c,
                                          const sparsepr_cache_attention_params* a,

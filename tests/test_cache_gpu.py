@@ -14,6 +14,18 @@ F16 = U.HALF[torch.float16]  # weights are rounded to 11 bits at least
 Q32 = 2.0 ** -11             # fp32 queries too
 
 
+def weights(rows):
+    """Half a step of the weights' type: fp16 while the cache is read in place
+    (up to 64 query rows per key head), bf16 beyond."""
+    return F16 if rows <= 64 else U.HALF[torch.bfloat16]
+
+
+def rounding(rows, dtype):
+    """Rounding of the queries: none for bf16 values; fp32 goes to 11 bits, beyond
+    64 rows to bf16."""
+    return 0.0 if dtype == torch.bfloat16 else Q32 if rows <= 64 else U.HALF[torch.bfloat16]
+
+
 def cache_params(B, Hkv, d, page, n_pages, max_pages):
     return dict(B=B, Hkv=Hkv, d=d, page=page, n_pages=n_pages, max_pages=max_pages)
 
@@ -71,8 +83,9 @@ class Run:
             n = attn["Nq"] if n_q is None else n_q[b]
             ref = F.attention(U.f64(q[b]), self.m.tokens(b, "k"), self.m.tokens(b, "v"), n, see,
                               attn.get("scale", 0.0))
-            U.check(out[b, :, :n], lse[b, :, :n], ref, dtype, p["d"], F16,
-                    qk_round=Q32 if dtype == torch.float32 else 0.0, what=(what, b))
+            rows = attn["Hq"] // p["Hkv"] * attn["Nq"]
+            U.check(out[b, :, :n], lse[b, :, :n], ref, dtype, p["d"], weights(rows),
+                    qk_round=rounding(rows, dtype), what=(what, b))
             assert (out[b, :, n:] == 7).all() and (lse[b, :, n:] == 7).all()
         return U.status(ws)
 
@@ -308,20 +321,21 @@ def test_evicted_pages_are_not_read():
     r.same()
     r.grow([1, 1])
     assert r.attend(dict(Hq=3, Nq=1, **see)) == 0
-    # a query that would look at them: reported, the rest is attended to
-    a = dict(Hq=1, Nq=1)
-    ws = S.allocate_cache_workspace(p, a)
-    q = U.normal((2, 1, 1, 64), 1)
-    out = torch.zeros_like(q)
-    S.sparsepr_cache_attention(q, p, r.c, a, out, ws)
-    assert U.status(ws) == 1 << S.ERR_INVALID_ARG
-    for b in range(2):
-        k, v = r.m.tokens(b, "k"), r.m.tokens(b, "v")
-        on = ~np.isnan(k[0, :, 0])
-        ref = F.attention(U.f64(q[b]), k[:, on], v[:, on], 1, dict(frame=1, window=0, sinks=0,
-                                                                  causal=1))
-        tol, _ = U.bounds(ref, q.dtype, 64, F16, 0.0, 0.0)
-        assert (np.abs(U.f64(out[b]) - ref["out"]) <= tol).all()
+    # queries that would look at them: reported, and NaN; those that do not are as they were
+    for Nq in (1, 70):
+        a = dict(Hq=1, Nq=Nq, frame=5, window=25, sinks=2)
+        ws = S.allocate_cache_workspace(p, a)
+        q = U.normal((2, 1, Nq, 64), 1)
+        out = torch.zeros_like(q)
+        S.sparsepr_cache_attention(q, p, r.c, a, out, ws)
+        assert U.status(ws) == 1 << S.ERR_INVALID_ARG
+        for b in range(2):
+            k, v = r.m.tokens(b, "k"), r.m.tokens(b, "v")
+            ref = F.attention(U.f64(q[b]), k, v, Nq, dict(frame=5, window=25, sinks=2, causal=1))
+            lost = np.isnan(ref["out"]).any(-1)
+            assert lost.any() and np.isnan(U.f64(out[b])[lost]).all()
+            tol, _ = U.bounds(ref, q.dtype, 64, weights(Nq), 0.0, 0.0)
+            assert (np.abs(U.f64(out[b]) - ref["out"])[~lost] <= tol[~lost]).all()
 
 
 def test_scales_far_apart():

@@ -190,6 +190,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   using L = Smem<HD>;
   constexpr int kAtoms = HD / 64;
   const WindowArgs& a = p.a;
+  // the combine kernel, if there is one, may be put in place; it waits for all blocks
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // block = (unit, split); segments vary fastest, and with a causal visibility the
   // last rows of all segments, which see the most, come first
   int bid = blockIdx.x;
@@ -697,45 +699,48 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // out = sum_s 2^(l_s - M) O_s / sum_s 2^(l_s - M), M = max_s l_s, over the splits'
 // normalised partial outputs in a fixed order; a split without any of the
-// row's keys has l_s = -inf and is not read. Thread = (row, 4 columns).
-template <typename T>
+// row's keys has l_s = -inf and weight 0. A warp per row: the lanes take one
+// split's log-sum-exp each, then HD / 32 columns each.
+template <int HD, typename T>
 __global__ void __launch_bounds__(256) window_combine_kernel(const WindowKernelParams p) {
+  constexpr int kC = HD / 32;
   const WindowArgs& a = p.a;
-  const int d = a.d, cpr = d / 4;
+  const int lane = threadIdx.x & 31;
   const int unit = blockIdx.y, seg = unit / p.tiles, tile = unit % p.tiles;
-  const int r = blockIdx.x * (256 / cpr) + threadIdx.x / cpr, c = (threadIdx.x % cpr) * 4;
-  const int r0 = tile * p.unit_rows;
+  const int r = blockIdx.x * 8 + (threadIdx.x >> 5), r0 = tile * p.unit_rows;
   const int bh0 = p.R != a.Nq ? seg * p.group : seg;
   const int n = clamp_count(a.n_q, bh0 / a.Hq, a.Nq, a.Nq, a.stats, false);
   if (r0 + r >= p.R || r >= p.unit_rows || (r0 + r) % a.Nq >= n) return;
   const size_t base = static_cast<size_t>(unit) * p.splits * p.unit_rows + r;
-  float M = -INFINITY;
-  bool nan = false;
+  const size_t row = static_cast<size_t>(bh0) * a.Nq + r0 + r;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // all of the attention kernel's writes
+  static_assert(kMaxWindowSplits <= 32, "a lane per split");
+  const float l = lane < p.splits ? p.lpart[base + static_cast<size_t>(lane) * p.unit_rows] : -INFINITY;
+  float M = l;
+#pragma unroll
+  for (int w = 16; w > 0; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
+  const bool nan = __any_sync(0xffffffffu, l != l);
+  const float weight = l == -INFINITY ? 0.f : exp2f(l - M);
+  float num[kC] = {}, den = 0.f;
+#pragma unroll 4
   for (int s = 0; s < p.splits; ++s) {
-    const float l = p.lpart[base + static_cast<size_t>(s) * p.unit_rows];
-    M = fmaxf(M, l);
-    nan = nan || l != l;
-  }
-  float num[4] = {0.f, 0.f, 0.f, 0.f}, den = 0.f;
-  for (int s = 0; s < p.splits; ++s) {
-    const size_t at = base + static_cast<size_t>(s) * p.unit_rows;
-    const float l = p.lpart[at];
-    if (l == -INFINITY) continue;
-    const float w = exp2f(l - M);
-    const float4 o = *reinterpret_cast<const float4*>(p.opart + at * d + c);
-    num[0] = fmaf(w, o.x, num[0]);
-    num[1] = fmaf(w, o.y, num[1]);
-    num[2] = fmaf(w, o.z, num[2]);
-    num[3] = fmaf(w, o.w, num[3]);
-    den += w;
+    const float w = __shfl_sync(0xffffffffu, weight, s);
+    const float* o = p.opart + (base + static_cast<size_t>(s) * p.unit_rows) * HD + lane * kC;
+    float v[kC];
+#pragma unroll
+    for (int e = 0; e < kC; ++e) v[e] = o[e];
+    if (w != 0.f) {  // a range without a key of the row may not have written its part
+      den += w;
+#pragma unroll
+      for (int e = 0; e < kC; ++e) num[e] = fmaf(w, v[e], num[e]);
+    }
   }
   const float inv = den > 0.f || nan ? 1.f / den : 0.f;
-  const size_t row = static_cast<size_t>(bh0) * a.Nq + r0 + r;
-  T* o = static_cast<T*>(a.out) + row * d + c;
+  T* out = static_cast<T*>(a.out) + row * HD + lane * kC;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) store_f32(o + e, num[e] * inv);
-  if (a.lse && c == 0)
-    a.lse[row] = nan ? num[0] * 0.f + den : den > 0.f ? (M + log2f(den)) * kLn2F : -INFINITY;
+  for (int e = 0; e < kC; ++e) store_f32(out + e, num[e] * inv);
+  if (a.lse && lane == 0)
+    a.lse[row] = nan ? den : den > 0.f ? (M + log2f(den)) * kLn2F : -INFINITY;
 }
 
 bool make_map2(CUtensorMap* m, const void* base, size_t rows, int d, int box_rows) {
@@ -775,12 +780,19 @@ cudaError_t launch_hd(const WindowKernelParams& p, const WindowMaps& maps, int u
   if (e != cudaSuccess) return e;
   window_attn_kernel<HD, T><<<static_cast<unsigned>(units) * p.splits, kThreads, kSmemBytes,
                               st>>>(maps, p);
-  if (p.splits > 1) {
-    const int rows = 256 / (HD / 4);
-    const dim3 grid((p.unit_rows + rows - 1) / rows, units);
-    window_combine_kernel<T><<<grid, 256, 0, st>>>(p);
-  }
-  return cudaGetLastError();
+  e = cudaGetLastError();
+  if (e != cudaSuccess || p.splits == 1) return e;
+  // launched beside the tail of the attention kernel (programmatic dependent launch)
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((min(p.unit_rows, p.R) + 7) / 8, units);
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, window_combine_kernel<HD, T>, p);
 }
 
 }  // namespace
@@ -788,38 +800,50 @@ cudaError_t launch_hd(const WindowKernelParams& p, const WindowMaps& maps, int u
 // How the rows are cut, from the sizes alone.
 //   - Short query runs of heads that share a key head are packed into one tile:
 //     their rows are contiguous, and the tile's 128 rows are filled.
-//   - Units of 256 rows (two tiles, each key tile read once for both) unless
-//     that leaves multiprocessors without a unit; then units of 128 rows.
-//   - With fewer units than multiprocessors the key tiles of a unit are split
-//     over several blocks, at least two tiles each, and joined afterwards.
+//   - Units have 256 rows (two tiles, each key tile read once for both) or 128, and
+//     the key tiles of a unit may be split over several blocks that are joined
+//     afterwards: whichever the estimate below holds for fastest. One block runs
+//     per multiprocessor, so a grid takes as many rounds as its blocks fill
+//     multiprocessors, the last one as long as a full one. A key tile costs 1 for
+//     256 rows and 0.6 for 128 (measured 1.7 us and 1.0 us), a block 4 beside its
+//     tiles, partial results what their bytes take at 6.5 TB/s, and the
+//     combine kernel 2. (A frame of 1,560 rows and 12 heads against 21,840 keys:
+//     156 units of 128 rows are two rounds, 371 us; 84 of 256 rows in 7 splits four
+//     rounds of a seventh.)
 WindowPlan window_plan(int B, int Hq, int Hkv, int Nq, int Nk, const sparsepr_visibility& see) {
   WindowPlan w = {};
   const int group = Hq / Hkv;
   const bool pack = group > 1 && Nq < kTileM;
   w.R = pack ? group * Nq : Nq;
   w.segs = pack ? B * Hkv : B * Hq;
-  w.unit_rows = 2 * kTileM;
-  w.tiles = (w.R + w.unit_rows - 1) / w.unit_rows;
-  if (w.R <= kTileM || static_cast<long long>(w.segs) * w.tiles < kPlanSMs) {
-    w.unit_rows = kTileM;
-    w.tiles = (w.R + w.unit_rows - 1) / w.unit_rows;
-  }
-  const long long units = static_cast<long long>(w.segs) * w.tiles;
-  w.splits = 1;
-  if (units < kPlanSMs) {
+  double best = 0.0;
+  for (int rows = 2 * kTileM; rows >= kTileM; rows -= kTileM) {
+    if (rows > kTileM && w.R <= kTileM) continue;
+    const long long tiles = (w.R + rows - 1) / rows, units = tiles * w.segs;
     long long keys = Nk;
     if (see.window > 0) {
       const long long F = see.frame;
-      const long long span = (see.sinks + (see.causal ? 1ll : 2ll) * see.window + 1) * F + w.unit_rows;
+      const long long span = (see.sinks + (see.causal ? 1ll : 2ll) * see.window + 1) * F + rows;
       if (span < keys) keys = span;
     }
     const long long key_tiles = (keys + kTileN - 1) / kTileN;
-    long long s = kPlanSMs / units;
-    if (s > kMaxWindowSplits) s = kMaxWindowSplits;
-    if (s > key_tiles / 2) s = key_tiles / 2;
-    if (s > 1) w.splits = static_cast<int>(s);
+    for (int splits = 1; splits <= kMaxWindowSplits && splits <= (key_tiles > 1 ? key_tiles : 1);
+         ++splits) {
+      const long long blocks = units * splits;
+      if (splits > 1 && blocks > 16 * kPlanSMs) break;
+      const long long rounds = (blocks + kPlanSMs - 1) / kPlanSMs;
+      const long long part = (key_tiles + splits - 1) / splits;
+      double cost = rounds * (part * (rows > kTileM ? 1.0 : 0.6) + 4.0);
+      if (splits > 1) cost += 2.0 + static_cast<double>(blocks) * rows * 1024 / (6.5e6 * 1.7);
+      if (w.unit_rows == 0 || cost < best) {
+        best = cost;
+        w.unit_rows = rows;
+        w.tiles = static_cast<int>(tiles);
+        w.units = static_cast<int>(units);
+        w.splits = splits;
+      }
+    }
   }
-  w.units = static_cast<int>(units);
   return w;
 }
 

@@ -496,6 +496,11 @@ def _ptr(t, name, shape, dtype, dev):
     raise ValueError("%s must be on the device of the workspace" % name)
 
 
+# the current stream's handle without a Stream object around it, where torch has that
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _launch(where: str, fn, args, ws, dev, stream):
     """One library call on the device of its tensors and, unless a stream is
     given, on that device's current stream."""
@@ -503,7 +508,7 @@ def _launch(where: str, fn, args, ws, dev, stream):
         _ws(ws)
     wp, wb = ws.data_ptr(), ws.numel()
     if dev < 0 or dev == torch.cuda.current_device():
-        st = (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+        st = _current_stream(dev) if stream is None else stream.cuda_stream
         code = fn(*args, wp, wb, st)
     else:
         with torch.cuda.device(dev):

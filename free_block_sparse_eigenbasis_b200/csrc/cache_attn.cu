@@ -84,22 +84,25 @@ struct DecodeParams {
 };
 
 // Tiles that the queries of a sequence need: 0..TA-1, then from TB on.
+template <int HD>
 struct SeqTiles {
+  static constexpr int kTile = tile_keys(HD);
   int L, n;        // keys, queries
   int SA, LB, HB;  // keys that some query sees: [0, SA) and [LB, HB)
-  int tile;        // keys of a tile
   int TA, TB, T;
-  __device__ int start(int t) const { return (t < TA ? t : TB + (t - TA)) * tile; }
+  __device__ int start(int t) const { return (t < TA ? t : TB + (t - TA)) * kTile; }
   // index of the tile that holds a visible key
   __device__ int tile_of(int j) const {
-    const int x = j / tile;
+    const int x = j / kTile;
     return x < TA ? x : TA + (x - TB);
   }
 };
 
-__device__ __forceinline__ SeqTiles seq_tiles(const CacheAttnArgs& a, int b, bool report) {
+template <int HD>
+__device__ __forceinline__ SeqTiles<HD> seq_tiles(const CacheAttnArgs& a, int b, bool report) {
+  constexpr int kTile = tile_keys(HD);
   const CacheArgs& c = a.cache;
-  SeqTiles s;
+  SeqTiles<HD> s;
   s.n = clamp_count(a.n_q, b, a.Nq, a.Nq, c.stats, report);
   s.L = clamp_count(c.c.len, b, c.p.max_pages * c.p.page, 0, c.stats, report);
   s.SA = s.LB = s.HB = 0;
@@ -111,11 +114,10 @@ __device__ __forceinline__ SeqTiles seq_tiles(const CacheAttnArgs& a, int b, boo
     s.LB = first.lo;
     s.HB = max(last.hi, s.LB);
   }
-  const int tile = tile_keys(c.p.d);
-  s.tile = tile;
-  s.TA = (s.SA + tile - 1) / tile;
-  s.TB = max(s.LB / tile, s.TA);
-  s.T = s.TA + max((s.HB + tile - 1) / tile - s.TB, 0);
+  // (non-negative: shifts, and no division at run time)
+  s.TA = static_cast<int>((static_cast<uint32_t>(s.SA) + kTile - 1) / kTile);
+  s.TB = max(static_cast<int>(static_cast<uint32_t>(s.LB) / kTile), s.TA);
+  s.T = s.TA + max(static_cast<int>((static_cast<uint32_t>(s.HB) + kTile - 1) / kTile) - s.TB, 0);
   return s;
 }
 
@@ -126,7 +128,7 @@ struct PagedKV {
   const CacheArgs& a;
   const int32_t* row;
   int h;
-  SeqTiles s;
+  SeqTiles<D> s;
   int t0, t1;
   __device__ bool ok(int j) const {
     const int t = s.tile_of(j);
@@ -196,11 +198,14 @@ __device__ __forceinline__ float log2_of_scale(float s) {
 // The block that holds flattened tile x of `total` when block c takes
 // [c total / blocks, (c + 1) total / blocks).
 __device__ __forceinline__ int owner(long long x, long long total, int blocks) {
+  if (total < (1 << 22))
+    return static_cast<int>((static_cast<uint32_t>(x + 1) * static_cast<uint32_t>(blocks) - 1) /
+                            static_cast<uint32_t>(total));
   return static_cast<int>(((x + 1) * blocks - 1) / total);
 }
 __device__ __forceinline__ int blocks_for(long long total) {
-  const long long want = (total + kMinTiles - 1) / kMinTiles;
-  return static_cast<int>(want < kDecodeBlocks ? (want > 0 ? want : 1) : kDecodeBlocks);
+  if (total >= static_cast<long long>(kDecodeBlocks) * kMinTiles) return kDecodeBlocks;
+  return max(1, (static_cast<int>(total) + kMinTiles - 1) / kMinTiles);
 }
 
 // Few query rows. The tiles of all (sequence, key head, 8 or 16 query rows)
@@ -257,7 +262,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
   int carry = 0;
   for (int b0 = 0; b0 < B; b0 += kDecodeThreads) {
     const int b = b0 + tid;
-    const int mine = b < B ? seq_tiles(a, b, blockIdx.x == 0).T : 0;
+    const int mine = b < B ? seq_tiles<HD>(a, b, blockIdx.x == 0).T : 0;
     int x = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -275,18 +280,24 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
     if (b < B) {
       pre[b] = before;
       if (blockIdx.x == 0) p.pre[b] = before;
+      if (b == B - 1) {
+        pre[B] = carry;
+        if (blockIdx.x == 0) p.pre[B] = carry;
+      }
     }
     __syncthreads();
   }
-  if (tid == 0) {
-    pre[B] = carry;
-    if (blockIdx.x == 0) p.pre[B] = carry;
-  }
-  __syncthreads();
   const long long total = static_cast<long long>(carry) * p.units_seq;
   const int blocks = blocks_for(total);
   if (total == 0 || static_cast<int>(blockIdx.x) >= blocks) return;
-  const long long begin = total * blockIdx.x / blocks, end = total * (blockIdx.x + 1) / blocks;
+  long long begin, end;
+  if (total < (1 << 22)) {  // 32-bit divisions; there are under 2^10 blocks
+    begin = static_cast<uint32_t>(total) * blockIdx.x / static_cast<uint32_t>(blocks);
+    end = static_cast<uint32_t>(total) * (blockIdx.x + 1) / static_cast<uint32_t>(blocks);
+  } else {
+    begin = total * blockIdx.x / blocks;
+    end = total * (blockIdx.x + 1) / blocks;
+  }
   volatile int* abort = &ms.abort;
 
   // the run of one unit inside [begin, end)
@@ -321,7 +332,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
   };
   struct Fetch {
     Run r;
-    SeqTiles s;
+    SeqTiles<HD> s;
     int h, count, batch;  // key head, tiles of this warp, first tile of `now`
     Look now, next;
     float ks0, vs0;       // scales of the batch before `now`, whose last tiles are still in use
@@ -379,8 +390,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
   };
   auto begin_run = [&](long long pos) {
     f.r = run_at(pos);
-    f.s = seq_tiles(a, f.r.b, false);
-    f.h = f.r.x / p.row_tiles;
+    f.s = seq_tiles<HD>(a, f.r.b, false);
+    f.h = p.row_tiles == 1 ? f.r.x : f.r.x / p.row_tiles;
     const int n = f.r.t1 - f.r.t0;
     f.count = warp < n ? (n - warp + kWarps - 1) / kWarps : 0;
     f.batch = 0;
@@ -400,11 +411,12 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
     // than 2 in magnitude (exact for bf16 values unless they lie 2^14 below the
     // row's largest). Thread = (row, 1 / 8 of its columns).
     uint2* const qs = reinterpret_cast<uint2*>(merge);  // [NT][kSteps][32]
-    auto put_queries = [&](const Run& r, const SeqTiles& s, int h) {
+    auto put_queries = [&](const Run& r, const SeqTiles<HD>& s, int h) {
       constexpr int kC = HD / 8;  // 16 or 8 columns a thread: a chunk, or half of one
       for (int x0 = tid & ~7; x0 < kRows * 8; x0 += kDecodeThreads) {
         const int rr = x0 >> 3, piece = tid & 7;
-        const int row = (r.x % p.row_tiles) * kRows + rr, i = row % a.Nq;
+        const int row = p.row_tiles == 1 ? rr : (r.x % p.row_tiles) * kRows + rr;
+        const int i = a.Nq == 1 ? 0 : row % a.Nq;
         const bool have = row < p.R && i < s.n;
         float x[kC], top = 0.f;
         if (have) {
@@ -456,8 +468,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
     sync();
     for (long long pos = begin; pos < end;) {
       const Run r = f.r;
-      const SeqTiles s = f.s;
-      const int h = f.h, row0 = (r.x % p.row_tiles) * kRows;
+      const SeqTiles<HD> s = f.s;
+      const int h = f.h, row0 = p.row_tiles == 1 ? 0 : (r.x % p.row_tiles) * kRows;
       const size_t q_base = (static_cast<size_t>(r.b) * a.Hq + static_cast<size_t>(h) * p.group) *
                                 a.Nq + row0;  // of q, out, lse: rows are contiguous
       float qf[NT][2];   // rows 2 t + e + 8 nt of this lane: logit = accumulator * qf * k_scale
@@ -892,7 +904,7 @@ __global__ void __launch_bounds__(256)
     widen_kernel(const CacheAttnArgs a, int b0, int cap, __nv_bfloat16* kb, __nv_bfloat16* vb) {
   const CacheArgs& c = a.cache;
   const int h = blockIdx.y, b = b0 + blockIdx.z;
-  const SeqTiles s = seq_tiles(a, b, false);
+  const SeqTiles<HD> s = seq_tiles<HD>(a, b, false);
   if (static_cast<int>(blockIdx.x) >= s.T) return;
   constexpr int kPieces = 4096 / 16;  // 16-byte pieces of the tile's keys, one per thread
   static_assert(kPieces == 256, "threads");

@@ -24,6 +24,10 @@ __host__ __device__ inline Range visible_range(const sparsepr_visibility& see, l
                                                long long L) {
   Range r = {0, 0, 0};
   if (p < 0 || L <= 0) return r;
+  if (see.window == 0 && see.frame == 1) {  // every key, or every key up to its own
+    r.hi = static_cast<int>(see.causal && p + 1 < L ? p + 1 : L);
+    return r;
+  }
   const long long F = see.frame;
   const long long f = see.frame == 1 ? p : static_cast<uint32_t>(p) / static_cast<uint32_t>(see.frame);
   long long end = L;  // keys a causal query may look at

@@ -12,27 +12,47 @@ namespace {
 constexpr int kPlanThreads = 1024;  // one block plans; a thread per sequence (B <= 1024)
 constexpr int kMinScaleExp = -110;
 
-// Exclusive prefix sum of v over the block; total in every thread.
-__device__ __forceinline__ long long block_scan(long long v, long long* warp_sums,
-                                                long long* total) {
+// Exclusive prefix sum of v over the kPlanThreads threads of the block, the total
+// in every thread. Calls alternate between two sets of warp sums, so one barrier
+// a call is enough.
+template <typename I>
+struct PlanScan {
+  I sums[2][32];
+};
+template <typename I>
+__device__ __forceinline__ I block_scan(I v, PlanScan<I>& sc, int& turn, I* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long x = v;
+  I x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    const I y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
-  __syncthreads();  // the sums of the last scan have been read
-  if (lane == 31) warp_sums[warp] = x;
+  if (lane == 31) sc.sums[turn][warp] = x;
   __syncthreads();
-  long long before = 0, all = 0;
-  for (int w = 0; w < static_cast<int>(blockDim.x) / 32; ++w) {
-    const long long s = warp_sums[w];
-    if (w < warp) before += s;
-    all += s;
+  I w = sc.sums[turn][lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const I y = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += y;
   }
-  *total = all;
-  return before + x - v;
+  turn ^= 1;
+  *total = __shfl_sync(0xffffffffu, w, 31);
+  const I before = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
+  return (warp ? before : 0) + x - v;
+}
+
+constexpr int kPerThread = 4;  // pages of a thread in one round over the pool
+constexpr int kRound = kPlanThreads * kPerThread;
+
+// ref of this thread's pages of a round, contiguous; past the pool: -1
+__device__ __forceinline__ void load_refs(const int32_t* ref, int n_pages, int base,
+                                          int (&r)[kPerThread]) {
+#pragma unroll
+  for (int e = 0; e < kPerThread; ++e) {
+    const int id = base + static_cast<int>(threadIdx.x) * kPerThread + e;
+    r[e] = id < n_pages ? ref[id] : -1;
+  }
 }
 
 __device__ __forceinline__ bool page_ok(const CacheArgs& a, int id) {
@@ -41,8 +61,11 @@ __device__ __forceinline__ bool page_ok(const CacheArgs& a, int id) {
 
 __global__ void __launch_bounds__(kPlanThreads)
     reserve_kernel(const CacheArgs a, const int32_t* n_new, int32_t* start) {
-  __shared__ long long warp_sums[32];
+  __shared__ PlanScan<long long> scan64;
+  __shared__ PlanScan<int> scan32;
   __shared__ int first[kPlanThreads + 1];  // first new page of each sequence
+  int turn64 = 0, turn32 = 0;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int b = threadIdx.x, page = a.p.page;
   const bool mine = b < a.p.B;
   const long long room = static_cast<long long>(a.p.max_pages) * page;
@@ -72,17 +95,23 @@ __global__ void __launch_bounds__(kPlanThreads)
   bad = __syncthreads_or(bad);
   full = __syncthreads_or(full);
   long long total;
-  const long long before = block_scan(need, warp_sums, &total);
+  const long long before = block_scan(need, scan64, turn64, &total);
   if (total > a.p.n_pages) full = true;
   // the first `total` free pages, ascending
   long long found = 0;
   if (!bad && !full)
-    for (int base = 0; base < a.p.n_pages && found < total; base += kPlanThreads) {
-      const int id = base + b;
-      const bool is_free = id < a.p.n_pages && a.c.ref[id] == 0;
-      long long here;
-      const long long at = found + block_scan(is_free ? 1 : 0, warp_sums, &here);
-      if (is_free && at < total) a.pages[at] = id;
+    for (long long base = 0; base < a.p.n_pages && found < total; base += kRound) {
+      int r[kPerThread], mine_free = 0, here;
+      load_refs(a.c.ref, a.p.n_pages, static_cast<int>(base), r);
+#pragma unroll
+      for (int e = 0; e < kPerThread; ++e) mine_free += r[e] == 0;
+      long long at = found + block_scan(mine_free, scan32, turn32, &here);
+#pragma unroll
+      for (int e = 0; e < kPerThread; ++e)
+        if (r[e] == 0) {
+          if (at < total) a.pages[at] = static_cast<int>(base) + b * kPerThread + e;
+          ++at;
+        }
       found += here;
     }
   if (found < total) full = true;
@@ -122,14 +151,27 @@ __global__ void __launch_bounds__(kPlanThreads)
   }
 }
 
-// 16-byte pieces [i0, i1) of page src to page dst, keys or values
+constexpr int kCopyThreads = 256, kCopyPieces = 1024;  // 16 KB of one page per block
+
+// 16-byte pieces [i0, i0 + kCopyPieces) of page src to page dst, keys or values: four
+// loads in flight per thread
 __device__ __forceinline__ void copy_pieces(const CacheArgs& a, const void* pool, long long src,
-                                            long long dst, int i0, int i1) {
-  const long long pieces = static_cast<long long>(a.p.Hkv) * a.p.page * a.p.d / 16;
+                                            long long dst, int i0) {
+  constexpr int kEach = kCopyPieces / kCopyThreads;
+  const int pieces = a.p.Hkv * (a.p.page * a.p.d / 16);
   const uint4* from = static_cast<const uint4*>(pool) + src * pieces;
   uint4* to = static_cast<uint4*>(const_cast<void*>(pool)) + dst * pieces;
-  for (int i = i0 + static_cast<int>(threadIdx.x); i < i1; i += static_cast<int>(blockDim.x))
-    to[i] = from[i];
+  uint4 x[kEach];
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    const int i = i0 + e * kCopyThreads + static_cast<int>(threadIdx.x);
+    if (i < pieces) x[e] = __ldcs(from + i);
+  }
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    const int i = i0 + e * kCopyThreads + static_cast<int>(threadIdx.x);
+    if (i < pieces) __stcs(to + i, x[e]);
+  }
 }
 __device__ __forceinline__ void copy_scales(const CacheArgs& a, long long src, long long dst) {
   for (int h = threadIdx.x; h < a.p.Hkv; h += blockDim.x) {
@@ -138,15 +180,12 @@ __device__ __forceinline__ void copy_scales(const CacheArgs& a, long long src, l
   }
 }
 
-constexpr int kCopyThreads = 256, kCopyPieces = 1024;  // 16 KB of one page per block
-
 __global__ void __launch_bounds__(kCopyThreads) copy_last_pages_kernel(const CacheArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan
   const int b = blockIdx.y, src = a.copies[b];
   if (src < 0) return;
   const int dst = a.copies[a.p.B + b];
-  const int pieces = a.p.Hkv * (a.p.page * a.p.d / 16);
-  const int i0 = blockIdx.x * kCopyPieces, i1 = min(i0 + kCopyPieces, pieces);
-  copy_pieces(a, blockIdx.z ? a.c.v8 : a.c.k8, src, dst, i0, i1);
+  copy_pieces(a, blockIdx.z ? a.c.v8 : a.c.k8, src, dst, blockIdx.x * kCopyPieces);
   if (blockIdx.x == 0 && blockIdx.z == 0) copy_scales(a, src, dst);
 }
 
@@ -216,36 +255,56 @@ __global__ void __launch_bounds__(128) evict_kernel(const CacheArgs a, sparsepr_
 // Plan of the packing: counts[0] moves, pages[i] -> targets[i].
 __global__ void __launch_bounds__(kPlanThreads)
     compact_plan_kernel(const CacheArgs a, int32_t* n_used) {
-  __shared__ long long warp_sums[32];
+  __shared__ PlanScan<int> scan;
+  __shared__ PlanScan<long long> scan64;
+  int turn = 0, turn64 = 0;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int n_pages = a.p.n_pages, tid = threadIdx.x;
   int mine = 0;
+#pragma unroll 4
   for (int id = tid; id < n_pages; id += kPlanThreads) mine += a.c.ref[id] > 0;
-  long long used;
-  block_scan(mine, warp_sums, &used);
-  long long holes = 0, moves = 0;
-  for (int base = 0; base < n_pages; base += kPlanThreads) {
-    const int id = base + tid;
-    const bool in_use = id < n_pages && a.c.ref[id] > 0;
-    const bool hole = id < used && !in_use, move = id >= used && in_use;
-    long long all;
-    // both counts in one scan: they stay below 2^31
-    const long long at = block_scan((static_cast<long long>(move) << 32) | (hole ? 1 : 0),
-                                    warp_sums, &all);
-    if (hole) a.targets[holes + (at & 0xffffffffll)] = id;
-    if (move) a.pages[moves + (at >> 32)] = id;
-    holes += all & 0xffffffffll;
-    moves += all >> 32;
+  int used;
+  block_scan(mine, scan, turn, &used);
+  int holes = 0, moves = 0;
+  int r[kPerThread];
+  load_refs(a.c.ref, n_pages, 0, r);
+  for (long long base = 0; base < n_pages; base += kRound) {
+    int next[kPerThread];
+    const bool more = base + kRound < n_pages;
+    if (more) load_refs(a.c.ref, n_pages, static_cast<int>(base + kRound), next);
+    // both counts in one scan, 32 bits each
+    long long count = 0, all;
+#pragma unroll
+    for (int e = 0; e < kPerThread; ++e) {
+      const int id = static_cast<int>(base) + tid * kPerThread + e;
+      if (r[e] == 0 && id < used) count += 1;
+      if (r[e] > 0 && id >= used) count += 1ll << 32;
+    }
+    const long long at = block_scan(count, scan64, turn64, &all);
+    int hole = holes + static_cast<int>(at & 0xffffffffll), move = moves + static_cast<int>(at >> 32);
+#pragma unroll
+    for (int e = 0; e < kPerThread; ++e) {
+      const int id = static_cast<int>(base) + tid * kPerThread + e;
+      if (r[e] == 0 && id < used) a.targets[hole++] = id;
+      if (r[e] > 0 && id >= used) a.pages[move++] = id;
+    }
+    holes += static_cast<int>(all & 0xffffffffll);
+    moves += static_cast<int>(all >> 32);
+    if (more)
+#pragma unroll
+      for (int e = 0; e < kPerThread; ++e) r[e] = next[e];
   }
   __syncthreads();
   for (int i = tid; i < moves; i += kPlanThreads) a.remap[a.pages[i]] = a.targets[i];
   if (tid == 0) {
-    a.counts[0] = static_cast<int32_t>(moves);
-    a.counts[1] = static_cast<int32_t>(used);
-    *n_used = static_cast<int32_t>(used);
+    a.counts[0] = moves;
+    a.counts[1] = used;
+    *n_used = used;
   }
 }
 
 __global__ void __launch_bounds__(kCopyThreads) compact_move_kernel(const CacheArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan
   const int moves = a.counts[0], used = a.counts[1];
   const long long entries = static_cast<long long>(a.p.B) * a.p.max_pages;
   for (long long i = static_cast<long long>(blockIdx.x) * kCopyThreads + threadIdx.x; i < entries;
@@ -263,8 +322,7 @@ __global__ void __launch_bounds__(kCopyThreads) compact_move_kernel(const CacheA
     const int part = static_cast<int>(w % parts), kv = static_cast<int>(w / parts) & 1;
     const int i = static_cast<int>(w / (2 * parts));
     const int src = a.pages[i], dst = a.targets[i];
-    copy_pieces(a, kv ? a.c.v8 : a.c.k8, src, dst, part * kCopyPieces,
-                min((part + 1) * kCopyPieces, pieces));
+    copy_pieces(a, kv ? a.c.v8 : a.c.k8, src, dst, part * kCopyPieces);
     if (part == 0 && kv == 0) {
       copy_scales(a, src, dst);
       if (threadIdx.x == 0) {
@@ -376,13 +434,31 @@ __global__ void __launch_bounds__(kAppendThreads)
 
 }  // namespace
 
+namespace {
+// A kernel that may be put in place while the one before it ends (it waits for
+// it with griddepcontrol.wait).
+template <typename... P>
+cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t st, P... p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p...);
+}
+}  // namespace
+
 cudaError_t launch_cache_reserve(const CacheArgs& a, const int32_t* n_new, int32_t* start,
                                  cudaStream_t st) {
   reserve_kernel<<<1, kPlanThreads, 0, st>>>(a, n_new, start);
   const int pieces = a.p.Hkv * (a.p.page * a.p.d / 16);
   const dim3 grid((pieces + kCopyPieces - 1) / kCopyPieces, a.p.B, 2);
-  copy_last_pages_kernel<<<grid, kCopyThreads, 0, st>>>(a);
-  return cudaGetLastError();
+  const cudaError_t e = cudaGetLastError();
+  return e != cudaSuccess ? e : launch_dependent(copy_last_pages_kernel, grid, kCopyThreads, st, a);
 }
 
 cudaError_t launch_cache_append(const CacheArgs& a, const void* k, const void* v, bool bf16, int T,
@@ -413,8 +489,9 @@ cudaError_t launch_cache_evict(const CacheArgs& a, const sparsepr_visibility& se
 
 cudaError_t launch_cache_compact(const CacheArgs& a, int32_t* n_used, cudaStream_t st) {
   compact_plan_kernel<<<1, kPlanThreads, 0, st>>>(a, n_used);
-  compact_move_kernel<<<a.sm_count * 8, kCopyThreads, 0, st>>>(a);
-  return cudaGetLastError();
+  const cudaError_t e = cudaGetLastError();
+  return e != cudaSuccess ? e
+                          : launch_dependent(compact_move_kernel, dim3(a.sm_count * 8), kCopyThreads, st, a);
 }
 
 }  // namespace spr

@@ -544,14 +544,31 @@ def sparsepr_window_attention(q, k, v, p: dict, out, ws, lse=None, n_q=None, n_k
 
 def _cache(p: dict, c: Cache, ws):
     """(parameters, their reference, reference to the pointers, device)"""
-    prm, dev = make_cache_params(p), _device(ws)
-    pages, f32 = (prm.n_pages, prm.Hkv), torch.float32
-    pool = pages + (prm.page, prm.d)
-    ptr = CachePointers(
-        _ptr(c.k8, "k8", pool, F8, dev), _ptr(c.v8, "v8", pool, F8, dev),
-        _ptr(c.k_scale, "k_scale", pages, f32, dev), _ptr(c.v_scale, "v_scale", pages, f32, dev),
-        _ptr(c.table, "table", (prm.B, prm.max_pages), I32, dev),
-        _ptr(c.len, "len", (prm.B,), I32, dev), _ptr(c.ref, "ref", (prm.n_pages,), I32, dev))
+    B, H, d, page, N, mp = p["B"], p["Hkv"], p["d"], p["page"], p["n_pages"], p["max_pages"]
+    prm, dev = CacheParams(B, H, d, page, N, mp), _device(ws)
+    k8, v8, ks, vs, table, length, ref = (c.k8, c.v8, c.k_scale, c.v_scale, c.table, c.len, c.ref)
+    f32 = torch.float32
+    try:  # the checks of _ptr for all seven at once
+        fine = (k8.shape == v8.shape == (N, H, page, d) and ks.shape == vs.shape == (N, H)
+                and table.shape == (B, mp) and length.shape == (B,) and ref.shape == (N,)
+                and k8.dtype is F8 and v8.dtype is F8 and ks.dtype is f32 and vs.dtype is f32
+                and table.dtype is I32 and length.dtype is I32 and ref.dtype is I32
+                and k8.is_contiguous() and v8.is_contiguous() and ks.is_contiguous()
+                and vs.is_contiguous() and table.is_contiguous() and length.is_contiguous()
+                and ref.is_contiguous() and (dev >= 0 or _DEVICE_TYPE == "cpu")
+                and dev == k8.get_device() == v8.get_device() == ks.get_device()
+                == vs.get_device() == table.get_device() == length.get_device()
+                == ref.get_device())
+    except AttributeError:
+        fine = False
+    if not fine:
+        for t, name, shape, dtype in (
+                (k8, "k8", (N, H, page, d), F8), (v8, "v8", (N, H, page, d), F8),
+                (ks, "k_scale", (N, H), f32), (vs, "v_scale", (N, H), f32),
+                (table, "table", (B, mp), I32), (length, "len", (B,), I32), (ref, "ref", (N,), I32)):
+            _ptr(t, name, shape, dtype, dev)
+    ptr = CachePointers(k8.data_ptr(), v8.data_ptr(), ks.data_ptr(), vs.data_ptr(),
+                        table.data_ptr(), length.data_ptr(), ref.data_ptr())
     return prm, ctypes.byref(prm), ctypes.byref(ptr), dev
 
 

@@ -570,13 +570,16 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
 #pragma unroll
         for (int kt = 1; kt < kKt; ++kt) one_scale = one_scale && lv[kt] == lv[0];
         const bool plain = whole && k0 >= from && k0 + kTile <= to;  // the same in the whole warp
-        bool moved = false;
-        float nm[NT][2], nM[NT][2];
+        // The references m and M of a row (-inf: nothing seen) are maxima of an earlier
+        // tile; they move only when a value passes them by 2^60 (weights of l, fp32)
+        // or 2^12 (weights of the second product, fp16 up to 2^16).
+        float tm[NT][2], tM[NT][2];  // this lane's maxima
+        bool rise = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float tm = -INFINITY, tM = -INFINITY;
+            tm[nt][e] = tM[nt][e] = -INFINITY;
 #pragma unroll
             for (int kt = 0; kt < kKt; ++kt)
 #pragma unroll
@@ -589,27 +592,32 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
                   else seen[nt][e] = true;
                 }
                 acc[kt][nt][2 * x + e] = v;
-                tm = fmaxf(tm, v);
-                if (!one_scale) tM = fmaxf(tM, v + lv[kt]);
+                tm[nt][e] = fmaxf(tm[nt][e], v);
+                if (!one_scale) tM[nt][e] = fmaxf(tM[nt][e], v + lv[kt]);
               }
+            if (one_scale) tM[nt][e] = tm[nt][e] + lv[0];
             if (plain) seen[nt][e] = true;
-#pragma unroll
-            for (int w = 4; w < 32; w <<= 1) {
-              tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, w));
-              if (!one_scale) tM = fmaxf(tM, __shfl_xor_sync(0xffffffffu, tM, w));
-            }
-            if (one_scale) tM = tm + lv[0];
-            const float mn = fmaxf(m[nt][e], tm), Mn = fmaxf(M[nt][e], tM);
-            // -inf - -inf only where nothing has been seen: the sums are 0 then
-            nm[nt][e] = mn == -INFINITY ? 0.f : mn;
-            nM[nt][e] = Mn == -INFINITY ? 0.f : Mn;
-            l[nt][e] *= ex2_approx(m[nt][e] - nm[nt][e]);
-            af[nt][e] = ex2_approx(M[nt][e] - nM[nt][e]);
-            moved = moved || Mn != M[nt][e];
-            m[nt][e] = mn;
-            M[nt][e] = Mn;
+            rise = rise || tm[nt][e] > m[nt][e] + 60.f || tM[nt][e] > M[nt][e] + 12.f;
           }
-        if (__any_sync(0xffffffffu, moved)) {
+        if (__any_sync(0xffffffffu, rise)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float x = tm[nt][e], y = tM[nt][e];
+#pragma unroll
+              for (int w = 4; w < 32; w <<= 1) {
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, w));
+                y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, w));
+              }
+              x = fmaxf(m[nt][e], x);
+              y = fmaxf(M[nt][e], y);
+              // -inf only where nothing has been seen: the sums are 0 then
+              l[nt][e] *= x == -INFINITY ? 0.f : ex2_approx(m[nt][e] - x);
+              af[nt][e] = y == -INFINITY ? 0.f : ex2_approx(M[nt][e] - y);
+              m[nt][e] = x;
+              M[nt][e] = y;
+            }
 #pragma unroll
           for (int mt = 0; mt < kSteps; ++mt)
 #pragma unroll
@@ -617,6 +625,14 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
 #pragma unroll
               for (int e = 0; e < 4; ++e) o[mt][nt][e] *= af[nt][e & 1];
         }
+        float nm[NT][2], nM[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            nm[nt][e] = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
+            nM[nt][e] = M[nt][e] == -INFINITY ? 0.f : M[nt][e];
+          }
         // ---- weights and the second product, 16 keys at a time ----
 #pragma unroll
         for (int kt = 0; kt < kKt; ++kt) {

@@ -27,7 +27,10 @@ constexpr int kDecodeThreads = kWarps * 32;
 constexpr int kMaxRows = 16;         // query rows of a block at most: 8 for each NT
 constexpr int kDecodeBlocks = 296;   // two per multiprocessor: one streams while the other merges
 constexpr int kMinTiles = kWarps;    // tiles per block at least (each goes to another warp)
-constexpr int kWideRows = 64;        // query rows per key head beyond which pages are widened
+// Query rows per key head beyond which pages are widened. In place against widened,
+// 4 heads of 20,000 tokens, d = 128: 16 rows 33 and 39 us, 32 rows 34 and 39, 48 rows 49
+// and 39; 64 (sequence, head) pairs of 4,000 tokens: 56 and 68, 71 and 70, 81 and 70.
+constexpr int kWideRows = 32;
 constexpr int kDepth = 2;            // tiles of a warp: one in hand, one on its way
 
 // keys of a tile, at multiples of that in the sequence: 4 KB of keys and of values
@@ -78,6 +81,7 @@ struct DecodeParams {
   int row_tiles;   // ceil(R / rows)
   int units_seq;   // Hkv * row_tiles
   int sub_rows;    // min(page, tile): rows of one copy
+  int combine_rows;  // query rows of a block of the combine kernel: 1, 2, 4 or 8
   int* pre;        // [B + 1] in the workspace: tiles before each sequence (for the combine)
   float* opart;    // [B * units_seq + blocks, rows, HD]
   float* lpart;    // [B * units_seq + blocks, rows]
@@ -850,66 +854,93 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
   if (*abort && tid == 0) raise_status(c.stats, SPARSEPR_ERR_TIMEOUT);
 }
 
-// Joins the partial results of units that more than one block worked on, in the
-// order of the blocks, and writes the rows that see nothing. A warp per query
-// row: the lanes take one block's log-sum-exp each, then HD / 32 columns each.
+// Joins the partial results of units that more than one block worked on, and
+// writes the rows that see nothing. One block per (sequence, unit) and
+// combine_rows of its rows; the block's 8 warps share out the rows, and the warps of
+// a row share out the parts, then add up in a fixed order; lanes take HD / 32
+// columns each. A long history of one sequence is cut into up to 296 parts: with few
+// units a block takes one row (8 rows x 74 parts of 4 units: 28 us by one warp a
+// row, 17 us by a block a unit).
+constexpr int kCombineWarps = 8;
+
 template <int HD, int NT, typename T>
-__global__ void __launch_bounds__(NT* 256) cache_combine_kernel(const DecodeParams p) {
+__global__ void __launch_bounds__(kCombineWarps * 32) cache_combine_kernel(const DecodeParams p) {
   constexpr int kRows = 8 * NT, kC = HD / 32;
+  __shared__ float sums[kCombineWarps][32][kC + 1];
   const CacheAttnArgs& a = p.a;
   const int b = blockIdx.x / p.units_seq, x = blockIdx.x % p.units_seq;
+  const int h = x / p.row_tiles, row0 = (x % p.row_tiles) * kRows;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int per_row = kCombineWarps / p.combine_rows;  // warps of a row
+  const int rr = blockIdx.y * p.combine_rows + warp / per_row, sub = warp % per_row;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // all of the decode kernel's writes
   const int before = p.pre[b], tiles = p.pre[b + 1] - before, all = p.pre[a.cache.p.B];
-  const int h = x / p.row_tiles, row0 = (x % p.row_tiles) * kRows;
-  const int rr = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n = clamp_count(a.n_q, b, a.Nq, a.Nq, a.cache.stats, false);
-  if (row0 + rr >= p.R || (row0 + rr) % a.Nq >= n) return;
+  const bool valid = rr < kRows && row0 + rr < p.R && (row0 + rr) % a.Nq < n;
   const size_t row = (static_cast<size_t>(b) * a.Hq + static_cast<size_t>(h) * p.group) * a.Nq +
                      row0 + rr;
   float num[kC] = {};
-  float lse = -INFINITY, inv = 0.f;
+  float M = -INFINITY, den = 0.f;
+  bool nan = false;
   if (tiles > 0) {
     const long long total = static_cast<long long>(all) * p.units_seq;
     const int blocks = blocks_for(total);
     const long long at = static_cast<long long>(before) * p.units_seq + static_cast<long long>(x) * tiles;
     const int c0 = owner(at, total, blocks), c1 = owner(at + tiles - 1, total, blocks);
     if (c0 == c1) return;  // written whole
-    const size_t slot0 = (static_cast<size_t>(blockIdx.x) + c0) * kRows + rr;
     const int count = c1 - c0 + 1;
-    float M = -INFINITY, den = 0.f;
-    bool nan = false;
-    for (int i = lane; i < count; i += 32) {
-      const float l = p.lpart[slot0 + static_cast<size_t>(i) * kRows];
-      M = fmaxf(M, l);
-      nan = nan || l != l;
-    }
-#pragma unroll
-    for (int w = 16; w > 0; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
-    nan = __any_sync(0xffffffffu, nan);
-    const float zM = M == -INFINITY ? 0.f : M;
-    for (int i0 = 0; i0 < count; i0 += 32) {
-      float w = 0.f;
-      if (i0 + lane < count) w = exp2f(p.lpart[slot0 + static_cast<size_t>(i0 + lane) * kRows] - zM);
-      const int m = min(32, count - i0);
+    const size_t slot0 = (static_cast<size_t>(blockIdx.x) + c0) * kRows + rr;
+    if (valid) {
 #pragma unroll 4
-      for (int i = 0; i < m; ++i) {
-        const float wi = __shfl_sync(0xffffffffu, w, i);
-        const float* o = p.opart + (slot0 + static_cast<size_t>(i0 + i) * kRows) * HD + lane * kC;
-        den += wi;
-        // a part that holds none of the row's keys is 0
+      for (int i = lane; i < count; i += 32) {
+        const float l = p.lpart[slot0 + static_cast<size_t>(i) * kRows];
+        M = fmaxf(M, l);
+        nan = nan || l != l;
+      }
 #pragma unroll
-        for (int e = 0; e < kC; ++e) num[e] = fmaf(wi, o[e], num[e]);
+      for (int w = 16; w > 0; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
+      nan = __any_sync(0xffffffffu, nan);
+      const float zM = M == -INFINITY ? 0.f : M;
+      constexpr int kAhead = 8;  // parts in flight
+      for (int i0 = sub; i0 < count; i0 += kAhead * per_row) {
+        float w[kAhead], o[kAhead][kC];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const int i = i0 + k * per_row;
+          const size_t slot = slot0 + static_cast<size_t>(min(i, count - 1)) * kRows;
+          w[k] = i < count ? p.lpart[slot] : -INFINITY;
+#pragma unroll
+          for (int e = 0; e < kC; ++e) o[k][e] = p.opart[slot * HD + lane * kC + e];
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const float wk = exp2f(w[k] - zM);  // 0 for a part that holds none of the row's keys
+          den += wk;
+#pragma unroll
+          for (int e = 0; e < kC; ++e) num[e] = fmaf(wk, o[k][e], num[e]);
+        }
       }
     }
-    if (den > 0.f || nan) {
-      inv = 1.f / den;
-      lse = nan ? den : M + log2f(den);
+    if (per_row > 1) {
+#pragma unroll
+      for (int e = 0; e < kC; ++e) sums[warp][lane][e] = num[e];
+      sums[warp][lane][kC] = den;
+      __syncthreads();
+      if (sub != 0) return;
+      for (int w = 1; w < per_row; ++w) {
+#pragma unroll
+        for (int e = 0; e < kC; ++e) num[e] += sums[warp + w][lane][e];
+        den += sums[warp + w][lane][kC];
+      }
     }
   }
+  if (!valid || sub != 0) return;
+  const bool some = den > 0.f || nan;
+  const float inv = some ? 1.f / den : 0.f;
   T* out = static_cast<T*>(a.out) + row * HD + lane * kC;
 #pragma unroll
   for (int e = 0; e < kC; ++e) store_f32(out + e, num[e] * inv);
-  if (a.lse && lane == 0) a.lse[row] = lse * kLn2F;
+  if (a.lse && lane == 0) a.lse[row] = nan ? den : some ? (M + log2f(den)) * kLn2F : -INFINITY;
 }
 
 // Many query rows: the tokens that some query sees, widened to bf16 rows
@@ -982,8 +1013,9 @@ cudaError_t launch_decode(const DecodeParams& p, const DecodeMaps& maps, cudaStr
   if (e != cudaSuccess) return e;
   // launched beside the tail of the decode kernel (programmatic dependent launch)
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.a.cache.p.B * p.units_seq);
-  cfg.blockDim = dim3(NT * 256);
+  const int rows = min(p.rows, p.R);
+  cfg.gridDim = dim3(p.a.cache.p.B * p.units_seq, (rows + p.combine_rows - 1) / p.combine_rows);
+  cfg.blockDim = dim3(kCombineWarps * 32);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1081,6 +1113,9 @@ cudaError_t launch_cache_attention(const CacheAttnArgs& a, cudaStream_t st) {
   p.row_tiles = w.row_tiles;
   p.units_seq = a.cache.p.Hkv * w.row_tiles;
   p.sub_rows = min(a.cache.p.page, tile_keys(a.cache.p.d));
+  p.combine_rows = 1;
+  if (a.cache.p.B * p.units_seq >= kDecodeBlocks / 2)
+    while (p.combine_rows < 8 && p.combine_rows < min(p.rows, p.R)) p.combine_rows *= 2;
   p.pre = a.pre;
   p.opart = a.opart;
   p.lpart = a.lpart;

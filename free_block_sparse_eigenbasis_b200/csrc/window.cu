@@ -722,7 +722,7 @@ __global__ void __launch_bounds__(256) window_combine_kernel(const WindowKernelP
   const bool nan = __any_sync(0xffffffffu, l != l);
   const float weight = l == -INFINITY ? 0.f : exp2f(l - M);
   float num[kC] = {}, den = 0.f;
-#pragma unroll 4
+#pragma unroll 8
   for (int s = 0; s < p.splits; ++s) {
     const float w = __shfl_sync(0xffffffffu, weight, s);
     const float* o = p.opart + (base + static_cast<size_t>(s) * p.unit_rows) * HD + lane * kC;

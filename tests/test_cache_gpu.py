@@ -16,14 +16,14 @@ Q32 = 2.0 ** -11             # fp32 queries too
 
 def weights(rows):
     """Half a step of the weights' type: fp16 while the cache is read in place
-    (up to 64 query rows per key head), bf16 beyond."""
-    return F16 if rows <= 64 else U.HALF[torch.bfloat16]
+    (up to 32 query rows per key head), bf16 beyond."""
+    return F16 if rows <= 32 else U.HALF[torch.bfloat16]
 
 
 def rounding(rows, dtype):
     """Rounding of the queries: none for bf16 values; fp32 goes to 11 bits, beyond
-    64 rows to bf16."""
-    return 0.0 if dtype == torch.bfloat16 else Q32 if rows <= 64 else U.HALF[torch.bfloat16]
+    32 rows to bf16."""
+    return 0.0 if dtype == torch.bfloat16 else Q32 if rows <= 32 else U.HALF[torch.bfloat16]
 
 
 def cache_params(B, Hkv, d, page, n_pages, max_pages):

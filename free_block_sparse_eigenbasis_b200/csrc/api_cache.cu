@@ -137,7 +137,7 @@ size_t carve_cache_attention(const sparsepr_cache_params& p,
   w.at = carve_cache(p, base, &a->cache);
   if (q.Nq > 0) {
     const CacheAttnPlan plan = cache_attn_plan(p, q);
-    a->pre = w.take<int32_t>(p.B + 1);
+    a->pre = w.take<int32_t>(p.B + 2);
     a->opart = w.take<float>(plan.part_rows * p.d);
     a->lpart = w.take<float>(plan.part_rows);
     if (plan.wide) {

@@ -27,6 +27,10 @@ constexpr int kDecodeThreads = kWarps * 32;
 constexpr int kMaxRows = 16;         // query rows of a block at most: 8 for each NT
 constexpr int kDecodeBlocks = 296;   // two per multiprocessor: one streams while the other merges
 constexpr int kMinTiles = kWarps;    // tiles per block at least (each goes to another warp)
+// When no sequence has more tiles than this, blocks take whole units: a unit's run costs
+// about 5 us beside its tiles, so short ones are not cut, nor lined up in few blocks (48
+// units of one tile: 49 us when blocks took six tiles each, 18 us in 48 blocks).
+constexpr int kWholeTiles = 24;
 // Query rows per key head beyond which pages are widened. In place against widened,
 // 4 heads of 20,000 tokens, d = 128: 16 rows 33 and 39 us, 32 rows 34 and 39, 48 rows 49
 // and 39; 64 (sequence, head) pairs of 4,000 tokens: 56 and 68, 71 and 70, 81 and 70.
@@ -82,7 +86,8 @@ struct DecodeParams {
   int units_seq;   // Hkv * row_tiles
   int sub_rows;    // min(page, tile): rows of one copy
   int combine_rows;  // query rows of a block of the combine kernel: 1, 2, 4 or 8
-  int* pre;        // [B + 1] in the workspace: tiles before each sequence (for the combine)
+  bool always_whole; // no sequence can have more than kWholeTiles tiles: nothing to combine
+  int* pre;        // [B + 2] in the workspace, for the combine: tiles before each sequence, whole units
   float* opart;    // [B * units_seq + blocks, rows, HD]
   float* lpart;    // [B * units_seq + blocks, rows]
 };
@@ -262,12 +267,13 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
     ms.flags = 0;
     fence_barrier_init();
   }
-  // tiles before each sequence
-  int carry = 0;
+  // tiles before each sequence, and the most tiles of one
+  int carry = 0, longest = 0;
   for (int b0 = 0; b0 < B; b0 += kDecodeThreads) {
     const int b = b0 + tid;
     const int mine = b < B ? seq_tiles<HD>(a, b, blockIdx.x == 0).T : 0;
     int x = mine;
+    longest = max(longest, mine);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, x, o);
@@ -291,8 +297,13 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
     }
     __syncthreads();
   }
-  const long long total = static_cast<long long>(carry) * p.units_seq;
-  const int blocks = blocks_for(total);
+  const bool whole_units = !__syncthreads_or(longest > kWholeTiles);
+  if (blockIdx.x == 0 && tid == 0) p.pre[B + 1] = whole_units;
+  // positions are units of the sequences in order, or tiles of them
+  const long long total = whole_units ? static_cast<long long>(B) * p.units_seq
+                                      : static_cast<long long>(carry) * p.units_seq;
+  const int blocks = whole_units ? static_cast<int>(min(total, static_cast<long long>(kDecodeBlocks)))
+                                 : blocks_for(total);
   if (total == 0 || static_cast<int>(blockIdx.x) >= blocks) return;
   long long begin, end;
   if (total < (1 << 22)) {  // 32-bit divisions; there are under 2^10 blocks
@@ -309,6 +320,14 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
     int b, x, t0, t1;  // sequence, unit of the sequence, tiles
   };
   auto run_at = [&](long long pos) {
+    if (whole_units) {
+      Run r;
+      r.b = static_cast<int>(pos / p.units_seq);
+      r.x = static_cast<int>(pos - static_cast<long long>(r.b) * p.units_seq);
+      r.t0 = 0;
+      r.t1 = pre[r.b + 1] - pre[r.b];
+      return r;
+    }
     int lo = 0, hi = B;  // pre[lo] * units <= pos < pre[hi] * units
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
@@ -325,6 +344,27 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
     r.t1 = static_cast<int>(min(static_cast<long long>(tiles), r.t0 + (end - pos)));
     return r;
   };
+  // the first position from pos on that has tiles; units without any are written here
+  auto with_tiles = [&](long long pos) {
+    if (whole_units)
+      for (; pos < end; ++pos) {
+        const Run r = run_at(pos);
+        if (r.t1 > 0) break;
+        const int h = r.x / p.row_tiles, row0 = (r.x % p.row_tiles) * kRows;
+        const int n = clamp_count(a.n_q, r.b, a.Nq, a.Nq, c.stats, false);
+        const size_t base = (static_cast<size_t>(r.b) * a.Hq + static_cast<size_t>(h) * p.group) *
+                                a.Nq + row0;
+        for (int x = tid; x < kRows * HD; x += kDecodeThreads) {
+          const int rr = x / HD;
+          if (row0 + rr >= p.R || (row0 + rr) % a.Nq >= n) continue;
+          store_f32(static_cast<T*>(a.out) + (base + rr) * HD + x % HD, 0.f);
+          if (a.lse && x % HD == 0) a.lse[base + rr] = -INFINITY;
+        }
+      }
+    return pos;
+  };
+  begin = with_tiles(begin);
+  if (begin >= end) return;
   const int sub = p.sub_rows, spp = kTile / sub;  // rows of a copy, copies of a tile: 1, 2, 4
   const int sub_shift = 31 - __clz(sub), page_shift = 31 - __clz(c.p.page);
   const int part = lane & (spp - 1), per_batch = 32 / spp;
@@ -695,7 +735,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
       }
       const bool full_unit = n_tiles == s.T;
       const size_t slot = static_cast<size_t>(r.b) * p.units_seq + r.x + blockIdx.x;
-      pos += n_tiles;
+      pos = with_tiles(pos + (whole_units ? 1 : n_tiles));
       if (pos < end) begin_run(pos);
       // ---- merge of the warps; those without a tile hold -inf, 0 ----
       const int used = min(n_tiles, kWarps);
@@ -875,6 +915,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) cache_combine_kernel(const
   const int rr = blockIdx.y * p.combine_rows + warp / per_row, sub = warp % per_row;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // all of the decode kernel's writes
   const int before = p.pre[b], tiles = p.pre[b + 1] - before, all = p.pre[a.cache.p.B];
+  if (p.pre[a.cache.p.B + 1]) return;  // blocks took whole units
   const int n = clamp_count(a.n_q, b, a.Nq, a.Nq, a.cache.stats, false);
   const bool valid = rr < kRows && row0 + rr < p.R && (row0 + rr) % a.Nq < n;
   const size_t row = (static_cast<size_t>(b) * a.Hq + static_cast<size_t>(h) * p.group) * a.Nq +
@@ -1005,12 +1046,13 @@ bool make_page_map(CUtensorMap* m, const void* base, const sparsepr_cache_params
 template <int HD, int NT, typename T>
 cudaError_t launch_decode(const DecodeParams& p, const DecodeMaps& maps, cudaStream_t st) {
   constexpr int kBytes = DecodeSmem<HD, NT>::bytes;
-  cudaError_t e = cudaFuncSetAttribute(cache_decode_kernel<HD, NT, T>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(cache_decode_kernel<HD, NT, T>), kBytes,
+                             allowed);
   if (e != cudaSuccess) return e;
   cache_decode_kernel<HD, NT, T><<<kDecodeBlocks, kDecodeThreads, kBytes, st>>>(maps, p);
   e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || p.always_whole) return e;
   // launched beside the tail of the decode kernel (programmatic dependent launch)
   cudaLaunchConfig_t cfg = {};
   const int rows = min(p.rows, p.R);
@@ -1113,6 +1155,16 @@ cudaError_t launch_cache_attention(const CacheAttnArgs& a, cudaStream_t st) {
   p.row_tiles = w.row_tiles;
   p.units_seq = a.cache.p.Hkv * w.row_tiles;
   p.sub_rows = min(a.cache.p.page, tile_keys(a.cache.p.d));
+  // tiles that a sequence can have at most: of its table row, or of what is visible
+  const sparsepr_visibility& see = a.see;
+  long long keys = static_cast<long long>(a.cache.p.max_pages) * a.cache.p.page;
+  if (see.window > 0) {
+    const long long F = see.frame;
+    const long long span = (see.sinks + (see.causal ? 1ll : 2ll) * see.window + 1) * F + a.Nq;
+    if (span < keys) keys = span;
+  }
+  // (a window may begin and the sinks may end inside a tile)
+  p.always_whole = keys / tile_keys(a.cache.p.d) + 4 <= kWholeTiles;
   p.combine_rows = 1;
   if (a.cache.p.B * p.units_seq >= kDecodeBlocks / 2)
     while (p.combine_rows < 8 && p.combine_rows < min(p.rows, p.R)) p.combine_rows *= 2;

@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "layout.h"
 
 namespace spr {
@@ -303,6 +305,19 @@ cudaError_t launch_correct(const float* o_sparse, const float* od, const int32_t
                            int N, int n_corr, int M, int d, void* out, bool out_bf16,
                            cudaStream_t st);
 
+// cudaFuncAttributeMaxDynamicSharedMemorySize of a kernel, set once per device;
+// `done` is the kernel's own set of devices (bit = device; beyond 64 every time).
+inline cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  const cudaError_t s = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (s == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return s;
+}
+
 // ---- window.cu: attention with a window of frames ---------------------------
 struct WindowArgs {
   const void *q, *k, *v;
@@ -365,7 +380,7 @@ struct CacheAttnArgs {
   float sc;  // scale * log2(e)
   bool bf16;
   // scratch in the workspace
-  int32_t* pre;          // [B + 1] tiles before each sequence
+  int32_t* pre;          // [B + 2] tiles before each sequence, whether blocks take whole units
   float *opart, *lpart;  // partial outputs and log2-sum-exps of units cut over blocks
   __nv_bfloat16 *qb, *kb, *vb;  // fp32 queries rounded to bf16, widened pages
 };

@@ -774,9 +774,9 @@ bool make_map3(CUtensorMap* m, const void* base, int heads, int rows, int d, int
 template <int HD, typename T>
 cudaError_t launch_hd(const WindowKernelParams& p, const WindowMaps& maps, int units,
                       cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(window_attn_kernel<HD, T>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       kSmemBytes);
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(window_attn_kernel<HD, T>), kSmemBytes,
+                             allowed);
   if (e != cudaSuccess) return e;
   window_attn_kernel<HD, T><<<static_cast<unsigned>(units) * p.splits, kThreads, kSmemBytes,
                               st>>>(maps, p);

@@ -27,10 +27,19 @@ constexpr int kDecodeThreads = kWarps * 32;
 constexpr int kMaxRows = 16;         // query rows of a block at most: 8 for each NT
 constexpr int kDecodeBlocks = 296;   // two per multiprocessor: one streams while the other merges
 constexpr int kMinTiles = kWarps;    // tiles per block at least (each goes to another warp)
-// When no sequence has more tiles than this, blocks take whole units: a unit's run costs
-// about 5 us beside its tiles, so short ones are not cut, nor lined up in few blocks (48
-// units of one tile: 49 us when blocks took six tiles each, 18 us in 48 blocks).
-constexpr int kWholeTiles = 24;
+// Blocks take whole units, or equal runs of tiles that may cut units, whichever is
+// estimated shorter: a unit's run costs about 5 us beside its tiles, a tile 2 us of its warp, and
+// the combine of cut units 4 us. (48 units of one tile: 49 us when 8 blocks took six tiles
+// each, 17 us in 48 blocks; 12 units of 11 tiles: 14.5 us whole, 21.5 us cut; 8 units of
+// 24 tiles: 20 us whole, 16.5 us cut.)
+constexpr int kWholeTiles = 16;  // units that cannot be longer are never cut
+__device__ __forceinline__ bool whole_is_shorter(int longest, long long tiles, long long units) {
+  const float b = kDecodeBlocks, u = static_cast<float>(units), t = static_cast<float>(tiles);
+  const float cut_blocks = fminf(b, fmaxf(1.f, t / kMinTiles));
+  const float whole = ceilf(u / b) * (5.f + 2.f * ceilf(static_cast<float>(longest) / kWarps));
+  const float cut = 5.f * (1.f + u / cut_blocks) + 2.f * ceilf(t / (cut_blocks * kWarps)) + 4.f;
+  return whole <= cut;
+}
 // Query rows per key head beyond which pages are widened. In place against widened,
 // 4 heads of 20,000 tokens, d = 128: 16 rows 33 and 39 us, 32 rows 34 and 39, 48 rows 49
 // and 39; 64 (sequence, head) pairs of 4,000 tokens: 56 and 68, 71 and 70, 81 and 70.
@@ -65,7 +74,7 @@ struct DecodeMisc {
   Range range[kMaxRows];                // of the run's query rows
   float q_scale[kMaxRows];
   int live[kMaxRows], valid[kMaxRows];  // the row sees a key; the row is in use
-  int warp_sums[kWarps];
+  int warp_sums[kWarps], warp_max[kWarps];
   uint32_t flags;
   int abort;
   float q[128];
@@ -86,7 +95,7 @@ struct DecodeParams {
   int units_seq;   // Hkv * row_tiles
   int sub_rows;    // min(page, tile): rows of one copy
   int combine_rows;  // query rows of a block of the combine kernel: 1, 2, 4 or 8
-  bool always_whole; // no sequence can have more than kWholeTiles tiles: nothing to combine
+  bool always_whole; // blocks take whole units whatever the lengths: nothing to combine
   int* pre;        // [B + 2] in the workspace, for the combine: tiles before each sequence, whole units
   float* opart;    // [B * units_seq + blocks, rows, HD]
   float* lpart;    // [B * units_seq + blocks, rows]
@@ -297,7 +306,15 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
     }
     __syncthreads();
   }
-  const bool whole_units = !__syncthreads_or(longest > kWholeTiles);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
+  if (lane == 0) ms.warp_max[warp] = longest;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) longest = max(longest, ms.warp_max[w]);
+  const bool whole_units =
+      p.always_whole || whole_is_shorter(longest, static_cast<long long>(carry) * p.units_seq,
+                                         static_cast<long long>(B) * p.units_seq);
   if (blockIdx.x == 0 && tid == 0) p.pre[B + 1] = whole_units;
   // positions are units of the sequences in order, or tiles of them
   const long long total = whole_units ? static_cast<long long>(B) * p.units_seq

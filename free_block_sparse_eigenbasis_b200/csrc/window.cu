@@ -705,6 +705,7 @@ template <int HD, typename T>
 __global__ void __launch_bounds__(256) window_combine_kernel(const WindowKernelParams p) {
   constexpr int kC = HD / 32;
   const WindowArgs& a = p.a;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // all of the attention kernel's writes
   const int lane = threadIdx.x & 31;
   const int unit = blockIdx.y, seg = unit / p.tiles, tile = unit % p.tiles;
   const int r = blockIdx.x * 8 + (threadIdx.x >> 5), r0 = tile * p.unit_rows;
@@ -713,7 +714,6 @@ __global__ void __launch_bounds__(256) window_combine_kernel(const WindowKernelP
   if (r0 + r >= p.R || r >= p.unit_rows || (r0 + r) % a.Nq >= n) return;
   const size_t base = static_cast<size_t>(unit) * p.splits * p.unit_rows + r;
   const size_t row = static_cast<size_t>(bh0) * a.Nq + r0 + r;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // all of the attention kernel's writes
   static_assert(kMaxWindowSplits <= 32, "a lane per split");
   const float l = lane < p.splits ? p.lpart[base + static_cast<size_t>(lane) * p.unit_rows] : -INFINITY;
   float M = l;

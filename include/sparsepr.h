@@ -430,7 +430,7 @@ typedef struct {
 
 typedef struct {
   int32_t B;    /* sequences */
-  int32_t Hq;   /* query heads, a multiple of Hkv */
+  int32_t Hq;   /* query heads, a multiple of Hkv; B * Hq <= 65535 */
   int32_t Hkv;  /* key / value heads; query head h reads key head h / (Hq / Hkv) */
   int32_t Nq;   /* query rows per sequence (0 is allowed) */
   int32_t Nk;   /* key rows per sequence (0 is allowed) */
@@ -486,7 +486,7 @@ typedef struct {
 } sparsepr_cache;
 
 typedef struct {
-  int32_t Hq;  /* query heads, a multiple of Hkv */
+  int32_t Hq;  /* query heads, a multiple of Hkv; B * Hq <= 65535 */
   int32_t Nq;  /* query rows per sequence (0 is allowed) */
   sparsepr_visibility see;
   double scale; /* softmax scale; 0 selects 1/sqrt(d) */

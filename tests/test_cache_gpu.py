@@ -370,6 +370,97 @@ def test_large_logits():
     assert r.attend(dict(Hq=4, Nq=40), scale=40.0) == 0
 
 
+def test_pools_beyond_32_bit_offsets():
+    """Pages whose bytes lie past 2^32 in the pool: append, copy of a shared last page,
+    attention in place and widened, packing back to the front."""
+    p = cache_params(3, 8, 128, 128, 34000, 3)  # 4.46 GB of keys, as much of values
+    c = S.allocate_cache(p)
+    c.ref[:33950] = 1  # all but the last pages are taken
+    ws, start = S.allocate_cache_workspace(p), U.i32([0] * 3)
+    n = U.i32([200, 0, 5])
+    S.sparsepr_cache_reserve(n, p, c, start, ws)
+    assert c.table[0].tolist() == [33950, 33951, -1] and c.table[2].tolist() == [33952, -1, -1]
+    k, v = U.normal((3, 8, 200, 128), 1), U.normal((3, 8, 200, 128), 2)
+    S.sparsepr_cache_append(k, v, p, c, start, n, ws)
+    S.sparsepr_cache_fork(U.i32([0]), U.i32([1]), p, c, ws)
+    one = U.i32([0, 1, 0])
+    S.sparsepr_cache_reserve(one, p, c, start, ws)  # sequence 1 gets a copy of page 33951
+    S.sparsepr_cache_append(k, v, p, c, start, one, ws)
+    assert c.table[1].tolist() == [33950, 33953, -1] and U.status(ws) == 0
+
+    def same_as_small():
+        """The same tokens in a small cache."""
+        small = Run(cache_params(3, 8, 128, 128, 8, 3))
+        small.start.copy_(U.i32([0, 0, 0]))
+        assert small.reserve([200, 201, 5])
+        kk, vv = (torch.cat([t[:1], torch.cat([t[:1], t[1:2, :, :1]], 2)[:, :, :201][:, :, :200],
+                             t[2:]]) for t in (k, v))
+        small.c.len.copy_(U.i32([0, 0, 0]))
+        S.sparsepr_cache_append(kk, vv, small.p, small.c, U.i32([0, 0, 0]), U.i32([200, 200, 5]),
+                                small.ws)
+        tail = [torch.zeros_like(t[:, :, :1]) for t in (k, v)]
+        for x, t in zip(tail, (k, v)):
+            x[1] = t[1, :, :1]
+        S.sparsepr_cache_append(tail[0].contiguous(), tail[1].contiguous(), small.p, small.c,
+                                U.i32([-1, 200, -1]), U.i32([0, 1, 0]), small.ws)
+        small.c.len.copy_(c.len)
+        for Nq in (1, 40):
+            a = dict(Hq=8, Nq=Nq)
+            q = U.normal((3, 8, Nq, 128), 5)
+            outs = []
+            for pp, cc in ((p, c), (small.p, small.c)):
+                out = torch.zeros_like(q)
+                w = S.allocate_cache_workspace(pp, a)
+                S.sparsepr_cache_attention(q, pp, cc, a, out, w)
+                assert U.status(w) == 0
+                outs.append(out)
+            assert torch.equal(outs[0], outs[1])
+
+    same_as_small()
+    c.ref[:33950] = 0  # and they are given up
+    used = U.i32([0])
+    S.sparsepr_cache_compact(p, c, used, ws)
+    assert int(used) == 4 and int(c.table.max()) == 3 and U.status(ws) == 0
+    same_as_small()
+
+
+def test_widened_pages_of_one_sequence_at_a_time():
+    """Table rows so long that the workspace holds the widened rows of one sequence."""
+    p = cache_params(3, 1, 64, 128, 12, 24000)
+    r = Run(p, 21)
+    r.grow([300, 129, 0])
+    attn = dict(Hq=1, Nq=40, window=150, sinks=2)
+    assert S.allocate_cache_workspace(p, attn).numel() < 900 * 2 ** 20
+    assert r.attend(attn) == 0
+    assert r.attend(attn, torch.float32, n_q=[40, 7, 3]) == 0
+
+
+def test_many_branches_of_one_history():
+    """1,024 sequences that share their pages: more tiles than 2^22, the same answer for
+    all of them."""
+    p = cache_params(1024, 32, 64, 16, 520, 520)
+    one = Run(dict(p, B=1), 3)
+    one.grow([8256])
+    c = S.allocate_cache(p)
+    for name in ("k8", "v8", "k_scale", "v_scale"):
+        getattr(c, name).view(torch.uint8).copy_(getattr(one.c, name).view(torch.uint8))
+    c.table[0], c.len[0] = one.c.table[0], one.c.len[0]
+    c.ref.copy_(one.c.ref)
+    ws = S.allocate_cache_workspace(p)
+    S.sparsepr_cache_fork(U.i32([0] * 1023), U.i32(list(range(1, 1024))), p, c, ws)
+    assert U.status(ws) == 0 and int(c.ref.max()) == 1024
+    q1 = U.normal((1, 32, 1, 64), 4)
+    outs = []
+    for pp, cc, q in ((one.p, one.c, q1), (p, c, q1.expand(1024, -1, -1, -1).contiguous())):
+        a = dict(Hq=32, Nq=1)
+        out, w = torch.zeros_like(q), S.allocate_cache_workspace(pp, a)
+        S.sparsepr_cache_attention(q, pp, cc, a, out, w)
+        assert U.status(w) == 0
+        outs.append(out.double())
+    # both round fp16 weights (2^-11 of values up to 0.5, over many tokens) and the output once
+    assert (outs[1] - outs[0]).abs().max() <= 2 * 2.0 ** -11 * 0.5 + 2.0 ** -8 * outs[0].abs().max()
+
+
 # ---- a run of them together -------------------------------------------------------
 def test_rollout_step_captured_and_replayed():
     """Prompt, then steps of reserve + append + attention captured once in a graph

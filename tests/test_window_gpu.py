@@ -204,6 +204,36 @@ def test_other_stream_graph_and_workspace_of_one_run():
     assert torch.equal(out2, want)
 
 
+def test_rows_beyond_32_bit_offsets():
+    """The last keys of a buffer of more than 2^32 bytes."""
+    N, W = 17_000_000, 300
+    k = torch.zeros((1, 1, N, 128), dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    k[:, :, -W:], v[:, :, -W:] = U.normal((1, 1, W, 128), 1), U.normal((1, 1, W, 128), 2)
+    q = U.normal((1, 2, 5, 128), 3)
+    p = params(1, 2, 1, 5, N, 128, window=200)
+    out, lse, st = call(p, q, k, v)
+    assert st == 0
+    ref = F.attention(U.f64(q[0]), U.f64(k[0, :, -W:]), U.f64(v[0, :, -W:]), 5, see(p))
+    U.check(out[0], lse[0], ref, q.dtype, 128, WEIGHTS)
+
+
+def test_calls_on_two_streams_with_workspaces_of_their_own():
+    p = params(2, 4, 2, 300, 400, 128, window=130, sinks=2)
+    q, k, v = inputs(p, torch.bfloat16, 31)
+    want, want_lse, _ = call(p, q, k, v)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [(torch.zeros_like(q), torch.zeros(q.shape[:3], device="cuda"),
+             S.allocate_window_workspace(p, q.dtype)) for _ in streams]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for st, (out, lse, ws) in zip(streams, outs):
+            S.sparsepr_window_attention(q, k, v, p, out, ws, lse=lse, stream=st)
+    torch.cuda.synchronize()
+    for out, lse, ws in outs:
+        assert torch.equal(out, want) and torch.equal(lse, want_lse) and U.status(ws) == 0
+
+
 def test_no_query_rows():
     p = params(1, 2, 1, 0, 10, 64)
     q, k, v = inputs(p, torch.bfloat16, 12)

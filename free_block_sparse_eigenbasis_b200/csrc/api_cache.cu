@@ -111,10 +111,8 @@ size_t carve_window(const sparsepr_window_params& p, sparsepr_dtype dt, char* ba
   }
   if (p.Nq > 0) {
     const WindowPlan plan = window_plan(p.B, p.Hq, p.Hkv, p.Nq, p.Nk, p.see);
-    const size_t rows = plan.splits > 1
-                            ? static_cast<size_t>(plan.units) * plan.splits * plan.unit_rows : 0;
-    a->opart = w.take<float>(rows * p.d);
-    a->lpart = w.take<float>(rows);
+    a->opart = w.take<float>(plan.part_rows * p.d);
+    a->lpart = w.take<float>(plan.part_rows);
   }
   return w.at;
 }

@@ -1103,9 +1103,7 @@ CacheAttnPlan cache_attn_plan(const sparsepr_cache_params& p, const sparsepr_cac
     for (int n : {w.group, p.B % w.group}) {
       if (n == 0) continue;
       const WindowPlan plan = window_plan(n, q.Hq, p.Hkv, q.Nq, w.cap, q.see);
-      const size_t rows = plan.splits > 1
-                              ? static_cast<size_t>(plan.units) * plan.splits * plan.unit_rows : 0;
-      if (rows > w.part_rows) w.part_rows = rows;
+      if (plan.part_rows > w.part_rows) w.part_rows = plan.part_rows;
     }
     return w;
   }

@@ -339,7 +339,9 @@ struct WindowPlan {
   int unit_rows;  // rows of a unit: 256 or 128
   int tiles;      // units per segment
   int units;      // segs * tiles
-  int splits;     // key ranges per unit
+  int whole;      // units of one block; the others are cut into
+  int splits;     // this many key ranges
+  size_t part_rows;  // rows of partial results
 };
 WindowPlan window_plan(int B, int Hq, int Hkv, int Nq, int Nk, const sparsepr_visibility& see);
 cudaError_t launch_window_attention(const WindowArgs& a, cudaStream_t st);

@@ -69,10 +69,11 @@ struct WindowKernelParams {
   int R, segs;         // rows per segment, segments (heads, or key heads with packed groups)
   int tiles;           // units per segment
   int unit_rows;       // 256 or 128
-  int splits;
+  int whole;           // the first units of the grid's order are one block each,
+  int splits;          // the others this many, which leave partial results
   int q_box_rows, kv_box_rows;
-  float* opart;        // [units, splits, unit_rows, d] normalised partial outputs
-  float* lpart;        // [units, splits, unit_rows] their log2-sum-exps
+  float* opart;        // [units - whole, splits, unit_rows, d] normalised partial outputs
+  float* lpart;        // [units - whole, splits, unit_rows] their log2-sum-exps
 };
 
 __device__ __forceinline__ void fma2(float& x0, float& x1, float a0, float a1, float b, float c) {
@@ -183,6 +184,15 @@ __device__ __forceinline__ void store_row32<__nv_bfloat16>(__nv_bfloat16* dst,
   }
 }
 
+// Segment and tile of the n-th unit of the grid: segments vary fastest, and with a
+// causal visibility the last rows of all segments, which see the most, come first.
+__device__ __forceinline__ void unit_place(const WindowKernelParams& p, int unit, int& seg,
+                                           int& tile) {
+  seg = unit % p.segs;
+  tile = unit / p.segs;
+  if (p.a.see.causal) tile = p.tiles - 1 - tile;
+}
+
 // T: the output type; the inputs are bf16.
 template <int HD, typename T>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -192,15 +202,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const WindowArgs& a = p.a;
   // the combine kernel, if there is one, may be put in place; it waits for all blocks
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  // block = (unit, split); segments vary fastest, and with a causal visibility the
-  // last rows of all segments, which see the most, come first
-  int bid = blockIdx.x;
-  const int split = bid % p.splits;
-  bid /= p.splits;
-  const int seg = bid % p.segs;
-  int tile = bid / p.segs;
-  if (a.see.causal) tile = p.tiles - 1 - tile;
-  const int unit = seg * p.tiles + tile;
+  // block = (unit, split)
+  const bool partial = static_cast<int>(blockIdx.x) >= p.whole && p.splits > 1;
+  const int splits = partial ? p.splits : 1;
+  const int cut = static_cast<int>(blockIdx.x) - p.whole;  // block among those of cut units
+  const int unit = partial ? p.whole + cut / splits : static_cast<int>(blockIdx.x);
+  const int split = partial ? cut % splits : 0;
+  int seg, tile;
+  unit_place(p, unit, seg, tile);
   const bool packed = p.R != a.Nq;  // the rows of all query heads of a key head
   const int bh0 = packed ? seg * p.group : seg;  // first (sequence, query head) of the segment
   const int b = bh0 / a.Hq;
@@ -236,12 +245,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   u.TA = (u.SA + kTileN - 1) / kTileN;
   const int T_all = u.TA + (u.HB - u.LB + kTileN - 1) / kTileN;
-  u.j0 = static_cast<int>(static_cast<long long>(T_all) * split / p.splits);
-  u.T = static_cast<int>(static_cast<long long>(T_all) * (split + 1) / p.splits) - u.j0;
+  u.j0 = static_cast<int>(static_cast<long long>(T_all) * split / splits);
+  u.T = static_cast<int>(static_cast<long long>(T_all) * (split + 1) / splits) - u.j0;
   const int T_tiles = u.T, j0 = u.j0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const bool partial = p.splits > 1;
-  const size_t pbase = (static_cast<size_t>(unit) * p.splits + split) * p.unit_rows;
+  const size_t pbase = partial ? static_cast<size_t>(cut) * p.unit_rows : 0;
   T* const out = static_cast<T*>(a.out);
 
   if (T_tiles == 0) {
@@ -707,12 +715,13 @@ __global__ void __launch_bounds__(256) window_combine_kernel(const WindowKernelP
   const WindowArgs& a = p.a;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // all of the attention kernel's writes
   const int lane = threadIdx.x & 31;
-  const int unit = blockIdx.y, seg = unit / p.tiles, tile = unit % p.tiles;
+  int seg, tile;
+  unit_place(p, p.whole + static_cast<int>(blockIdx.y), seg, tile);
   const int r = blockIdx.x * 8 + (threadIdx.x >> 5), r0 = tile * p.unit_rows;
   const int bh0 = p.R != a.Nq ? seg * p.group : seg;
   const int n = clamp_count(a.n_q, bh0 / a.Hq, a.Nq, a.Nq, a.stats, false);
   if (r0 + r >= p.R || r >= p.unit_rows || (r0 + r) % a.Nq >= n) return;
-  const size_t base = static_cast<size_t>(unit) * p.splits * p.unit_rows + r;
+  const size_t base = static_cast<size_t>(blockIdx.y) * p.splits * p.unit_rows + r;
   const size_t row = static_cast<size_t>(bh0) * a.Nq + r0 + r;
   static_assert(kMaxWindowSplits <= 32, "a lane per split");
   const float l = lane < p.splits ? p.lpart[base + static_cast<size_t>(lane) * p.unit_rows] : -INFINITY;
@@ -778,13 +787,14 @@ cudaError_t launch_hd(const WindowKernelParams& p, const WindowMaps& maps, int u
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(window_attn_kernel<HD, T>), kSmemBytes,
                              allowed);
   if (e != cudaSuccess) return e;
-  window_attn_kernel<HD, T><<<static_cast<unsigned>(units) * p.splits, kThreads, kSmemBytes,
-                              st>>>(maps, p);
+  const unsigned blocks = static_cast<unsigned>(p.whole) +
+                          static_cast<unsigned>(units - p.whole) * p.splits;
+  window_attn_kernel<HD, T><<<blocks, kThreads, kSmemBytes, st>>>(maps, p);
   e = cudaGetLastError();
-  if (e != cudaSuccess || p.splits == 1) return e;
+  if (e != cudaSuccess || p.whole == units) return e;
   // launched beside the tail of the attention kernel (programmatic dependent launch)
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((min(p.unit_rows, p.R) + 7) / 8, units);
+  cfg.gridDim = dim3((min(p.unit_rows, p.R) + 7) / 8, units - p.whole);
   cfg.blockDim = dim3(256);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -801,22 +811,22 @@ cudaError_t launch_hd(const WindowKernelParams& p, const WindowMaps& maps, int u
 //   - Short query runs of heads that share a key head are packed into one tile:
 //     their rows are contiguous, and the tile's 128 rows are filled.
 //   - Units have 256 rows (two tiles, each key tile read once for both) or 128, and
-//     the key tiles of a unit may be split over several blocks that are joined
-//     afterwards: whichever the estimate below holds for fastest. One block runs
-//     per multiprocessor, so a grid takes as many rounds as its blocks fill
-//     multiprocessors, the last one as long as a full one. A key tile costs 1 for
-//     256 rows and 0.6 for 128 (measured 1.7 us and 1.0 us), a block 4 beside its
-//     tiles, partial results what their bytes take at 6.5 TB/s, and the
-//     combine kernel 2. (A frame of 1,560 rows and 12 heads against 21,840 keys:
-//     156 units of 128 rows are two rounds, 371 us; 84 of 256 rows in 7 splits four
-//     rounds of a seventh.)
+//     the key tiles of the units that do not fill a last round of the multiprocessors,
+//     or of all units, may be split over several blocks that are joined afterwards:
+//     whichever the estimate below holds for fastest. One block runs per
+//     multiprocessor, so blocks take as many rounds as they fill multiprocessors, the
+//     last one as long as a full one. A key tile costs 1 for 256 rows and 0.6 for 128
+//     (measured 1.7 us and 1.0 us), a block 4 beside its tiles, partial results what
+//     their bytes take at 6.5 TB/s, and the combine kernel 2. (A frame of 1,560 rows and
+//     12 heads against 21,840 keys: 156 units of 128 rows are two rounds, 371 us; 84 of 256
+//     rows in 5 splits three rounds of a fifth, 279 us.)
 WindowPlan window_plan(int B, int Hq, int Hkv, int Nq, int Nk, const sparsepr_visibility& see) {
   WindowPlan w = {};
   const int group = Hq / Hkv;
   const bool pack = group > 1 && Nq < kTileM;
   w.R = pack ? group * Nq : Nq;
   w.segs = pack ? B * Hkv : B * Hq;
-  double best = 0.0;
+  double best = -1.0;
   for (int rows = 2 * kTileM; rows >= kTileM; rows -= kTileM) {
     if (rows > kTileM && w.R <= kTileM) continue;
     const long long tiles = (w.R + rows - 1) / rows, units = tiles * w.segs;
@@ -827,23 +837,38 @@ WindowPlan window_plan(int B, int Hq, int Hkv, int Nq, int Nk, const sparsepr_vi
       if (span < keys) keys = span;
     }
     const long long key_tiles = (keys + kTileN - 1) / kTileN;
-    for (int splits = 1; splits <= kMaxWindowSplits && splits <= (key_tiles > 1 ? key_tiles : 1);
-         ++splits) {
-      const long long blocks = units * splits;
-      if (splits > 1 && blocks > 16 * kPlanSMs) break;
-      const long long rounds = (blocks + kPlanSMs - 1) / kPlanSMs;
-      const long long part = (key_tiles + splits - 1) / splits;
-      double cost = rounds * (part * (rows > kTileM ? 1.0 : 0.6) + 4.0);
-      if (splits > 1) cost += 2.0 + static_cast<double>(blocks) * rows * 1024 / (6.5e6 * 1.7);
-      if (w.unit_rows == 0 || cost < best) {
-        best = cost;
-        w.unit_rows = rows;
-        w.tiles = static_cast<int>(tiles);
-        w.units = static_cast<int>(units);
-        w.splits = splits;
+    const double tile_cost = rows > kTileM ? 1.0 : 0.6;
+    const auto rounds = [&](long long blocks, long long part) {
+      return (blocks + kPlanSMs - 1) / kPlanSMs * (part * tile_cost + 4.0);
+    };
+    const long long full = units / kPlanSMs * kPlanSMs;  // units of full rounds
+    for (const long long whole : {units, full, 0ll}) {
+      for (int splits = 1; splits <= kMaxWindowSplits && splits <= key_tiles; ++splits) {
+        const long long cut = units - whole;
+        if ((cut == 0) != (splits == 1)) continue;  // something to split, or nothing
+        if (cut * splits > 16 * kPlanSMs) break;
+        double cost = rounds(whole, key_tiles);
+        if (cut > 0)
+          cost += rounds(cut * splits, (key_tiles + splits - 1) / splits) + 2.0 +
+                  static_cast<double>(cut * splits) * rows * 1024 / (6.5e6 * 1.7);
+        if (best < 0.0 || cost < best) {
+          best = cost;
+          w.unit_rows = rows;
+          w.tiles = static_cast<int>(tiles);
+          w.units = static_cast<int>(units);
+          w.whole = static_cast<int>(whole);
+          w.splits = splits;
+        }
       }
     }
+    if (best < 0.0) {  // no keys at all
+      w.unit_rows = rows;
+      w.tiles = static_cast<int>(tiles);
+      w.units = w.whole = static_cast<int>(units);
+      w.splits = 1;
+    }
   }
+  w.part_rows = static_cast<size_t>(w.units - w.whole) * w.splits * w.unit_rows;
   return w;
 }
 
@@ -858,6 +883,7 @@ cudaError_t launch_window_attention(const WindowArgs& in, cudaStream_t st) {
   p.segs = w.segs;
   p.tiles = w.tiles;
   p.unit_rows = w.unit_rows;
+  p.whole = w.whole;
   p.splits = w.splits;
   p.opart = a.opart;
   p.lpart = a.lpart;

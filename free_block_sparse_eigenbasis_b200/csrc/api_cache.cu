@@ -66,6 +66,9 @@ sparsepr_status check_cache_attention(const sparsepr_cache_params* p,
   if (!(isfinite(a->scale) && a->scale >= 0.0)) return SPARSEPR_ERR_INVALID_ARG;
   const long long bh = static_cast<long long>(p->B) * a->Hq;
   if (bh > kMaxHeads || bh * a->Nq > kMaxRows) return SPARSEPR_ERR_UNSUPPORTED;
+  // tiles of all sequences are counted in 32 bits
+  if (p->B * (static_cast<long long>(p->max_pages) * p->page / 32 + 4) > kMaxRows)
+    return SPARSEPR_ERR_UNSUPPORTED;
   return SPARSEPR_OK;
 }
 

@@ -229,8 +229,8 @@ __device__ __forceinline__ int blocks_for(long long total) {
 // Few query rows. The tiles of all (sequence, key head, 8 or 16 query rows)
 // units form one line that is cut evenly over the blocks, whatever the lengths:
 // a block takes a run of it, which may end one unit, hold several and begin
-// another. Of a run, warp w takes every 12th tile: it looks the pages up (32 at a
-// time, ahead), fetches keys and values by TMA into its own two stages and keeps
+// another; or blocks take whole units, where that is shorter (whole_is_shorter).
+// Of a run, warp w takes every 6th tile: it looks the pages up (32 at a time, ahead), fetches keys and values by TMA into its own two stages and keeps
 // its own running maxima, sum and accumulator in registers, so that warps do not
 // wait for one another (one warp that fetched for all was the bound: 3.3 TB/s).
 // The first tiles of the next run are fetched before the warps are merged at
@@ -246,6 +246,12 @@ __device__ __forceinline__ int blocks_for(long long total) {
 // columns (HD / 8) g .. The tile is swizzled by TMA, so that the lanes of a
 // quarter warp meet different banks. The weights are turned into the second
 // product's operand by an 8x8 transpose.
+//
+// Bound by the stream of pages where there is much to read (32 sequences of up to
+// 8,192 tokens, 8 key heads: 85.6 us, 4.3 TB/s; 72 us without the arithmetic), else by
+// latency: a block's run takes about 7 us around its first tiles (12 heads of 1,000 tokens:
+// 18.5 us with the combine). Two blocks of six warps hide one another's ends: one block of
+// twelve took 105 us.
 template <int HD, int NT, typename T>
 __global__ void __launch_bounds__(kDecodeThreads, 2)
     cache_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeParams p) {
@@ -386,7 +392,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
   const int sub_shift = 31 - __clz(sub), page_shift = 31 - __clz(c.p.page);
   const int part = lane & (spp - 1), per_batch = 32 / spp;
 
-  // ---- fetching: tile k of the warp is tile warp + 12 k of its run ----
+  // ---- fetching: tile k of the warp is tile warp + 6 k of its run ----
   struct Look {  // one copy: page (-1: none to fetch), first key, scales
     int id, key0;
     float ks, vs;  // ks < 0: no query sees these keys; NaN: the entry holds no page
@@ -1003,7 +1009,8 @@ __global__ void __launch_bounds__(kCombineWarps * 32) cache_combine_kernel(const
 
 // Many query rows: the tokens that some query sees, widened to bf16 rows
 // [sequence - b0, head, position, HD] (exact: 4 significant bits times a power of
-// two). One block per tile of a sequence and head.
+// two). One block per tile of a sequence and head. Bound by memory: 21,840 tokens of 12
+// heads, 67 MB to 134 MB, in 38 us (5.3 TB/s).
 template <int HD>
 __global__ void __launch_bounds__(256)
     widen_kernel(const CacheAttnArgs a, int b0, int cap, __nv_bfloat16* kb, __nv_bfloat16* vb) {
@@ -1011,6 +1018,14 @@ __global__ void __launch_bounds__(256)
   const int h = blockIdx.y, b = b0 + blockIdx.z;
   const SeqTiles<HD> s = seq_tiles<HD>(a, b, false);
   if (static_cast<int>(blockIdx.x) >= s.T) return;
+  if (static_cast<int>(blockIdx.x) == s.TA - 1) {
+    // the attention's tiles of 128 keys read on behind the sinks, with weight 0: no NaN there
+    const int from = s.TA * tile_keys(HD);
+    const int to = min(min((s.SA + kTileN - 1) / kTileN * kTileN, s.TB * tile_keys(HD)), cap);
+    uint4* v = reinterpret_cast<uint4*>(
+        vb + ((static_cast<size_t>(blockIdx.z) * c.p.Hkv + h) * cap + from) * HD);
+    for (int i = threadIdx.x; i < (to - from) * HD / 8; i += 256) v[i] = make_uint4(0, 0, 0, 0);
+  }
   constexpr int kPieces = 4096 / 16;  // 16-byte pieces of the tile's keys, one per thread
   static_assert(kPieces == 256, "threads");
   const int key = s.start(blockIdx.x) + threadIdx.x * 16 / HD, col = threadIdx.x * 16 % HD;
@@ -1018,8 +1033,8 @@ __global__ void __launch_bounds__(256)
   const int id = c.c.table[static_cast<size_t>(b) * c.p.max_pages + key / c.p.page];
   const size_t to = ((static_cast<size_t>(blockIdx.z) * c.p.Hkv + h) * cap + key) * HD + col;
   const bool page = id >= 0 && id < c.p.n_pages;
-  if (!page && (key < s.SA || (key >= s.LB && key < s.HB)))
-    raise_status(c.stats, SPARSEPR_ERR_INVALID_ARG);
+  const bool visible = key < s.SA || (key >= s.LB && key < s.HB);
+  if (!page && visible) raise_status(c.stats, SPARSEPR_ERR_INVALID_ARG);
   const size_t slot = static_cast<size_t>(page ? id : 0) * c.p.Hkv + h;
   const size_t from = (slot * c.p.page + key % c.p.page) * HD + col;
 #pragma unroll
@@ -1035,7 +1050,8 @@ __global__ void __launch_bounds__(256)
       u[0] = make_uint4(w[0], w[1], w[2], w[3]);
       u[1] = make_uint4(w[4], w[5], w[6], w[7]);
     } else {  // NaN: a query that needs the token shows it
-      u[0] = u[1] = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+      const uint32_t w = visible ? 0x7fff7fffu : 0u;
+      u[0] = u[1] = make_uint4(w, w, w, w);
     }
     uint4* dst = reinterpret_cast<uint4*>((kv ? vb : kb) + to);
     dst[0] = u[0];

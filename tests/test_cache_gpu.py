@@ -338,6 +338,41 @@ def test_evicted_pages_are_not_read():
             assert (np.abs(U.f64(out[b]) - ref["out"])[~lost] <= tol[~lost]).all()
 
 
+def test_what_lies_behind_the_sinks_does_not_matter():
+    """Widened pages: the rows between the sinks and the window are whatever the
+    workspace held."""
+    p = cache_params(2, 1, 64, 16, 80, 40)
+    r = Run(p, 17)
+    r.grow([600, 400])
+    see = dict(frame=1, window=100, sinks=20, causal=1)
+    attn = dict(Hq=1, Nq=50, **see)
+    S.sparsepr_cache_evict(dict(see, window=150), p, r.c, r.ws)
+    r.m.evict(1, 150, 20)
+    ws = S.allocate_cache_workspace(p, attn)
+    ws.fill_(0xFF)  # NaN in every type
+    S.sparsepr_reset_stats(ws)
+    assert r.attend(attn, ws=ws) == 0
+
+
+def test_first_call_inside_a_capture():
+    p = cache_params(1, 1, 64, 32, 8, 4)
+    r = Run(p, 19)
+    r.grow([100])
+    for Nq in (1, 40):
+        attn = dict(Hq=3, Nq=Nq)
+        q = U.normal((1, 3, Nq, 64), 2, torch.float32)
+        out, ws = torch.zeros_like(q), S.allocate_cache_workspace(p, attn)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            S.sparsepr_cache_attention(q, p, r.c, attn, out, ws)
+        g.replay()
+        torch.cuda.synchronize()
+        again = torch.zeros_like(q)
+        S.sparsepr_cache_attention(q, p, r.c, attn, again, ws)
+        assert U.status(ws) == 0 and torch.equal(out, again) and out.abs().sum() > 0
+
+
 def test_scales_far_apart():
     """Pages whose values differ by thirty powers of two, the weight on the
     small ones; keys likewise."""

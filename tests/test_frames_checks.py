@@ -104,6 +104,10 @@ def test_cache_call_arguments():
                 dict(causal=-1), dict(scale=float("inf"))):
         assert attend(bad) == S.ERR_INVALID_ARG, bad
     assert attend(dict(Nq=1 << 30)) == S.ERR_UNSUPPORTED
+    wide = ctypes.byref(S.make_cache_params(dict(CACHE, B=1024, max_pages=1 << 26)))
+    a = ctypes.byref(S.make_cache_attention_params(ATTN))
+    assert L.sparsepr_cache_workspace_bytes(wide, None) > 0
+    assert L.sparsepr_cache_workspace_bytes(wide, a) == 0  # more tiles than 2^31
     assert attend(q=None) == attend(out=None) == attend(out=FAKE) == S.ERR_INVALID_ARG
     assert attend(dt=5) == S.ERR_UNSUPPORTED
     assert attend(dict(Nq=0), q=None, out=None) == S.OK

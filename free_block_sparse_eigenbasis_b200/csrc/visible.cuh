@@ -15,13 +15,37 @@ struct Range {
   int s, lo, hi;
 };
 
+// Division of n < 2^31 by an invariant d >= 1, as a product, an addition and a shift
+// (Granlund and Montgomery, "Division by invariant integers using multiplication",
+// 1994): with l = ceil(log2 d) and m = floor(2^32 (2^l - d) / d) + 1,
+// n / d = (floor(m n / 2^32) + n) >> l; the sum stays below 2^32.
+struct Divider {
+  uint32_t d, mul, shift;
+  Divider() = default;
+  explicit Divider(int by) : d(static_cast<uint32_t>(by)), shift(0) {
+    while ((1ull << shift) < d) ++shift;
+    mul = static_cast<uint32_t>(((1ull << 32) * ((1ull << shift) - d)) / d + 1);
+  }
+  __device__ int div(int n) const {
+    return static_cast<int>((__umulhi(mul, static_cast<uint32_t>(n)) + n) >> shift);
+  }
+  __device__ int mod(int n) const { return n - div(n) * static_cast<int>(d); }
+};
+struct PlainDivision {
+  int d;
+  __host__ __device__ int div(int n) const {
+    return static_cast<int>(static_cast<uint32_t>(n) / static_cast<uint32_t>(d));
+  }
+};
+
 // Keys that the query at position p of a sequence of L keys sees. All three
 // ends grow with p, so the keys of a run of rows lie in [0, s of the last row)
 // and [lo of the first, hi of the last).
 // Positions and counts are below 2^31; only the products by the frame need
-// more, and divisions stay in 32 bits.
+// more, and divisions stay in 32 bits. by_frame divides by the frame.
+template <class Division>
 __host__ __device__ inline Range visible_range(const sparsepr_visibility& see, long long p,
-                                               long long L) {
+                                               long long L, const Division& by_frame) {
   Range r = {0, 0, 0};
   if (p < 0 || L <= 0) return r;
   if (see.window == 0 && see.frame == 1) {  // every key, or every key up to its own
@@ -29,7 +53,7 @@ __host__ __device__ inline Range visible_range(const sparsepr_visibility& see, l
     return r;
   }
   const long long F = see.frame;
-  const long long f = see.frame == 1 ? p : static_cast<uint32_t>(p) / static_cast<uint32_t>(see.frame);
+  const long long f = see.frame == 1 ? p : by_frame.div(static_cast<int>(p));
   long long end = L;  // keys a causal query may look at
   if (see.causal && (f + 1) * F < L) end = (f + 1) * F;
   long long s = see.sinks * F;
@@ -47,6 +71,10 @@ __host__ __device__ inline Range visible_range(const sparsepr_visibility& see, l
   r.hi = static_cast<int>(hi);
   if (r.hi < r.lo) r.hi = r.lo;
   return r;
+}
+__host__ __device__ inline Range visible_range(const sparsepr_visibility& see, long long p,
+                                               long long L) {
+  return visible_range(see, p, L, PlainDivision{see.frame});
 }
 
 // In-use rows of one sequence, clamped to what the buffers hold.

@@ -78,6 +78,9 @@ struct WindowKernelParams {
   int whole;           // the first units of the grid's order are one block each,
   int splits;          // the others this many, which leave partial results
   int q_box_rows, kv_box_rows;
+  // the kernel divides by these: some fifteen divisions at run time took 2,300 cycles
+  // at the start of every block
+  Divider by_segs, by_group, by_Hq, by_Nq, by_splits, by_frame;
   float* opart;        // [units - whole, splits, unit_rows, d] normalised partial outputs
   float* lpart;        // [units - whole, splits, unit_rows] their log2-sum-exps
 };
@@ -166,36 +169,53 @@ struct TileKV {
   }
 };
 
-template <typename T>
-__device__ __forceinline__ void store_row32(T* dst, const uint32_t (&o)[32], float f);
-template <>
-__device__ __forceinline__ void store_row32<float>(float* dst, const uint32_t (&o)[32], float f) {
-#pragma unroll
-  for (int k = 0; k < 32; k += 4)
-    *reinterpret_cast<float4*>(dst + k) =
-        make_float4(__uint_as_float(o[k]) * f, __uint_as_float(o[k + 1]) * f,
-                    __uint_as_float(o[k + 2]) * f, __uint_as_float(o[k + 3]) * f);
-}
-template <>
-__device__ __forceinline__ void store_row32<__nv_bfloat16>(__nv_bfloat16* dst,
-                                                           const uint32_t (&o)[32], float f) {
-#pragma unroll
-  for (int k = 0; k < 32; k += 8) {
-    uint4 u;
-    u.x = pack_bf16x2(__uint_as_float(o[k]) * f, __uint_as_float(o[k + 1]) * f);
-    u.y = pack_bf16x2(__uint_as_float(o[k + 2]) * f, __uint_as_float(o[k + 3]) * f);
-    u.z = pack_bf16x2(__uint_as_float(o[k + 4]) * f, __uint_as_float(o[k + 5]) * f);
-    u.w = pack_bf16x2(__uint_as_float(o[k + 6]) * f, __uint_as_float(o[k + 7]) * f);
-    *reinterpret_cast<uint4*>(dst + k) = u;
+// The 32 rows of a warp, half a row (HD / 2 columns) at a time, go to memory by
+// way of shared memory, so that a store instruction covers whole lines: a thread
+// that writes its own row touches 32 lines with each, 4,500 cycles a block at
+// d = 128. The 16-byte pieces of a row are swizzled against bank conflicts.
+template <typename T, int HD>
+struct RowStage {
+  static constexpr int kPer = 16 / static_cast<int>(sizeof(T));  // values of a piece
+  static constexpr int kPieces = HD / 2 / kPer;                  // of half a row: 4, 8 or 16
+  static __device__ __forceinline__ int at(int row, int piece) {
+    return row * kPieces + (piece ^ (kPieces >= 8 ? row & 7 : (row >> 1) & 3));
   }
-}
+  // 32 columns of the lane's row, the c32-th of its half, times f
+  static __device__ __forceinline__ void put(uint4* stage, int lane, int c32, const uint32_t (&o)[32],
+                                             float f) {
+#pragma unroll
+    for (int k = 0; k < 32; k += kPer) {
+      uint4 u;
+      uint32_t* w = &u.x;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int x = k + e * kPer / 4;
+        if constexpr (kPer == 4) w[e] = __float_as_uint(__uint_as_float(o[x]) * f);
+        else w[e] = pack_bf16x2(__uint_as_float(o[x]) * f, __uint_as_float(o[x + 1]) * f);
+      }
+      stage[at(lane, (c32 * 32 + k) / kPer)] = u;
+    }
+  }
+  // dst: the half's first column in the warp's first row; rows: the lanes whose rows are written
+  static __device__ __forceinline__ void flush(const uint4* stage, int lane, T* dst, uint32_t rows) {
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) {
+      const int x = j * 32 + lane, row = x / kPieces, piece = x % kPieces;
+      if ((rows >> row) & 1u)
+        *reinterpret_cast<uint4*>(dst + static_cast<size_t>(row) * HD + piece * kPer) =
+            stage[at(row, piece)];
+    }
+    __syncwarp();
+  }
+};
 
 // Segment and tile of the n-th unit of the grid: segments vary fastest, and with a
 // causal visibility the last rows of all segments, which see the most, come first.
 __device__ __forceinline__ void unit_place(const WindowKernelParams& p, int unit, int& seg,
                                            int& tile) {
-  seg = unit % p.segs;
-  tile = unit / p.segs;
+  tile = p.by_segs.div(unit);
+  seg = unit - tile * p.segs;
   if (p.a.see.causal) tile = p.tiles - 1 - tile;
 }
 
@@ -212,15 +232,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool partial = static_cast<int>(blockIdx.x) >= p.whole && p.splits > 1;
   const int splits = partial ? p.splits : 1;
   const int cut = static_cast<int>(blockIdx.x) - p.whole;  // block among those of cut units
-  const int unit = partial ? p.whole + cut / splits : static_cast<int>(blockIdx.x);
-  const int split = partial ? cut % splits : 0;
+  const int unit = partial ? p.whole + p.by_splits.div(cut) : static_cast<int>(blockIdx.x);
+  const int split = partial ? p.by_splits.mod(cut) : 0;
   int seg, tile;
   unit_place(p, unit, seg, tile);
   const bool packed = p.R != a.Nq;  // the rows of all query heads of a key head
   const int bh0 = packed ? seg * p.group : seg;  // first (sequence, query head) of the segment
-  const int b = bh0 / a.Hq;
-  const int kvh = b * a.Hkv + (bh0 % a.Hq) / p.group;
-  const bool report = split == 0 && tile == 0 && bh0 % a.Hq == 0 && threadIdx.x == 0;
+  const int b = p.by_Hq.div(bh0), head0 = bh0 - b * a.Hq;
+  const int kvh = b * a.Hkv + p.by_group.div(head0);
+  const bool report = split == 0 && tile == 0 && head0 == 0 && threadIdx.x == 0;
   const int n = clamp_count(a.n_q, b, a.Nq, a.Nq, a.stats, report);
   const int len = clamp_count(a.n_k, b, a.Nk, a.Nk, a.stats, report);
   const int r0 = tile * p.unit_rows;
@@ -228,8 +248,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int nq = rows_unit > kTileM ? 2 : 1;
   const size_t row_base = static_cast<size_t>(bh0) * a.Nq + r0;  // of q, out, lse
   // first and last query of the unit (packed rows wrap from head to head)
-  int i_first = r0 % a.Nq, i_last = (r0 + rows_unit - 1) % a.Nq;
-  if (r0 / a.Nq != (r0 + rows_unit - 1) / a.Nq) {
+  int i_first = p.by_Nq.mod(r0), i_last = p.by_Nq.mod(r0 + rows_unit - 1);
+  if (i_last - i_first != rows_unit - 1) {
     i_first = 0;
     i_last = a.Nq - 1;
   }
@@ -238,8 +258,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const long long pos0 = static_cast<long long>(len) - n;  // position of query 0
   UnitKeys u;
   {
-    const Range first = visible_range(a.see, max(pos0 + i_first, 0ll), len);
-    const Range last = visible_range(a.see, pos0 + i_last, len);
+    const Range first = visible_range(a.see, max(pos0 + i_first, 0ll), len, p.by_frame);
+    const Range last = visible_range(a.see, pos0 + i_last, len, p.by_frame);
     u.SA = last.s;
     u.LB = first.lo;
     u.HB = last.hi;
@@ -464,10 +484,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_tmem = tmem + lane_base + static_cast<uint32_t>(i * kTileN);
     const uint32_t o_base = tmem + lane_base + 2u * kTileN;
     const float sc = a.sc;
-    const int qi = (r0 + ur) % a.Nq;
+    const int qi = p.by_Nq.mod(r0 + ur);
     const bool valid = ur < rows_unit && qi < n;
     Range rg = {0, 0, 0};
-    if (valid) rg = visible_range(a.see, pos0 + qi, len);
+    if (valid) rg = visible_range(a.see, pos0 + qi, len, p.by_frame);
     // rows that nobody reads, and rows that see nothing, take every key unmasked
     // against the reference 0 and are dropped at the end
     const bool live = valid && (rg.s > 0 || rg.hi > rg.lo);
@@ -632,10 +652,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         p.lpart[pbase + ur] = -INFINITY;
       }
       bool finite = true;
-      constexpr int kCols = HD / 32;  // 32-column pieces of a row
+      constexpr int kHalf = HD / 64;  // 32-column pieces of half a row
+      const uint32_t rows = __ballot_sync(0xffffffffu, valid);
+      const int ur0 = ur - lane;  // the warp's first row
+      // the query tile has been read: a quarter of it for each warp
+      uint4* stage = reinterpret_cast<uint4*>(Qs + i * L::kTileBytes + (warp & 3) * (L::kTileBytes / 4));
 #pragma unroll
-      for (int c = 0; c < kCols; ++c) {
-        if (!two && (c / (kCols / 2)) != i) continue;
+      for (int c = 0; c < 2 * kHalf; ++c) {
+        if (!two && c / kHalf != i) continue;
         uint32_t o[32];
         tmem_ld32(o_base + (two ? i * HD : 0) + c * 32, o);
         tmem_wait_ld();
@@ -659,9 +683,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int k = 0; k < 32; ++k) o[k] = 0u;
         }
-        if (valid) {
-          if (partial) store_row32(p.opart + (pbase + ur) * HD + c * 32, o, f);
-          else store_row32(out + (row_base + ur) * HD + c * 32, o, f);
+        if (partial) RowStage<float, HD>::put(stage, lane, c % kHalf, o, f);
+        else RowStage<T, HD>::put(stage, lane, c % kHalf, o, f);
+        if (c % kHalf == kHalf - 1) {
+          const int col = c / kHalf * (HD / 2);
+          if (partial) RowStage<float, HD>::flush(stage, lane, p.opart + (pbase + ur0) * HD + col, rows);
+          else RowStage<T, HD>::flush(stage, lane, out + (row_base + ur0) * HD + col, rows);
         }
       }
       if (live && !finite) atomicOr(&flags[ur >> 5], 1u << (ur & 31));
@@ -694,7 +721,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         q[c] = load_f32(static_cast<const __nv_bfloat16*>(a.q) + row * HD + c);
       __syncthreads();
       float m, l, o;
-      literal_row<kThreads, HD>(kv, q, visible_range(a.see, pos0 + (r0 + ur) % a.Nq, len), a.sc,
+      literal_row<kThreads, HD>(kv, q, visible_range(a.see, pos0 + p.by_Nq.mod(r0 + ur), len, p.by_frame), a.sc,
                                 scratch, BlockSync{}, m, l, o);
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const float lsev = l == 0.f ? -INFINITY : m + log2f(l);
@@ -891,6 +918,12 @@ cudaError_t launch_window_attention(const WindowArgs& in, cudaStream_t st) {
   p.unit_rows = w.unit_rows;
   p.whole = w.whole;
   p.splits = w.splits;
+  p.by_segs = Divider(p.segs);
+  p.by_group = Divider(p.group);
+  p.by_Hq = Divider(a.Hq);
+  p.by_Nq = Divider(a.Nq);
+  p.by_splits = Divider(p.splits);
+  p.by_frame = Divider(a.see.frame);
   p.opart = a.opart;
   p.lpart = a.lpart;
   const size_t q_rows = static_cast<size_t>(a.B) * a.Hq * a.Nq;

@@ -55,7 +55,7 @@ constexpr int kSmemBytes = Smem<128>::bytes + 1024;
 static_assert(kSmemBytes <= static_cast<int>(kMaxDynSmem), "shared memory");
 
 struct Bars {
-  uint64_t q_full;
+  uint64_t q_full[2];
   uint64_t kfull[kStages], vfull[kStages], kempty[kStages], vempty[kStages];
   uint64_t vfix[2];
   uint64_t s_full[2], p_full[2][2], pa_done[2], o_done[2];
@@ -111,6 +111,10 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
       " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
       : "memory");
+}
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
 // one lane of the (converged) warp
@@ -228,6 +232,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const WindowArgs& a = p.a;
   // the combine kernel, if there is one, may be put in place; it waits for all blocks
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (threadIdx.x >= 8 * 32 && threadIdx.x < 8 * 32 + 3)
+    prefetch_map(threadIdx.x == 8 * 32 ? &maps.q : threadIdx.x == 8 * 32 + 1 ? &maps.k : &maps.v);
   // block = (unit, split)
   const bool partial = static_cast<int>(blockIdx.x) >= p.whole && p.splits > 1;
   const int splits = partial ? p.splits : 1;
@@ -271,8 +277,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   u.TA = (u.SA + kTileN - 1) / kTileN;
   const int T_all = u.TA + (u.HB - u.LB + kTileN - 1) / kTileN;
-  u.j0 = static_cast<int>(static_cast<long long>(T_all) * split / splits);
-  u.T = static_cast<int>(static_cast<long long>(T_all) * (split + 1) / splits) - u.j0;
+  u.j0 = 0;
+  u.T = T_all;
+  if (partial) {  // (fewer than 2^24 tiles and 16 splits)
+    u.j0 = p.by_splits.div(T_all * split);
+    u.T = p.by_splits.div(T_all * (split + 1)) - u.j0;
+  }
   const int T_tiles = u.T, j0 = u.j0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const size_t pbase = partial ? static_cast<size_t>(cut) * p.unit_rows : 0;
@@ -311,8 +321,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* ml = reinterpret_cast<float*>(smem + L::ml_off);
   uint32_t* flags = reinterpret_cast<uint32_t*>(smem + L::flag_off);
 
-  if (threadIdx.x == 0) {
-    mbar_init(&bars->q_full, 1);
+  if (threadIdx.x == 9 * 32) {  // while warp 0 takes tensor memory
+    mbar_init(&bars->q_full[0], 1);
+    mbar_init(&bars->q_full[1], 1);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&bars->kfull[s], 1);
       mbar_init(&bars->vfull[s], 1);
@@ -350,13 +361,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* empty = is_k ? bars->kempty : bars->vempty;
     const CUtensorMap* map = is_k ? &maps.k : &maps.v;
     const uint32_t bytes = kAtoms * p.kv_box_rows * 128;
-    if (is_k && lane == 0) {
-      mbar_arrive_expect_tx(&bars->q_full, nq * kAtoms * p.q_box_rows * 128);
-      for (int qt = 0; qt < nq; ++qt)
-        for (int c = 0; c < kAtoms; ++c)
-          tma_load_2d(Qs + qt * L::kTileBytes + c * L::kSlab, &maps.q, &bars->q_full, c * 64,
-                      static_cast<int32_t>(row_base) + qt * kTileM);
-    }
+    auto load_q = [&](int qt) {
+      mbar_arrive_expect_tx(&bars->q_full[qt], kAtoms * p.q_box_rows * 128);
+      for (int c = 0; c < kAtoms; ++c)
+        tma_load_2d(Qs + qt * L::kTileBytes + c * L::kSlab, &maps.q, &bars->q_full[qt], c * 64,
+                    static_cast<int32_t>(row_base) + qt * kTileM);
+    };
+    if (is_k && lane == 0) load_q(0);
     int issued = -1, fixes = 0;
     for (int j = 0; j < T_tiles; ++j) {
       const int st = j % kStages, k0 = u.start(j0 + j);
@@ -367,6 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive_expect_tx(&full[st], bytes);
           for (int c = 0; c < kAtoms; ++c)
             tma_load_3d(ring + st * L::kTileBytes + c * L::kSlab, map, &full[st], c * 64, k0, kvh);
+          if (is_k && j == 0 && two) load_q(1);  // needed after the first products of tile 0
         }
       }
       if (!__shfl_sync(0xffffffffu, ok, 0)) break;
@@ -389,7 +401,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       volatile int never = 0;
       for (int j = max(0, issued - kStages + 1); j <= issued; ++j)
         mbar_wait(&full[j % kStages], (j / kStages) & 1, &never);
-      if (is_k) mbar_wait(&bars->q_full, 0, &never);
+      if (is_k) {
+        mbar_wait(&bars->q_full[0], 0, &never);
+        if (two) mbar_wait(&bars->q_full[1], 0, &never);
+      }
     }
   } else if (warp == 9) {
     // ------------------------------ MMA issuer --------------------------------
@@ -403,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t k_desc = smem_desc_sw128(smem_u32(Ks), 16, 1024);
     const uint64_t v_desc = smem_desc_sw128(smem_u32(Vs), L::kSlab, 1024);
     const bool leader = elect_one();
-    bool ok = __all_sync(0xffffffffu, mbar_wait(&bars->q_full, 0, abort));
+    bool ok = true;
     auto kv_of = [&](int i, int t) { return two ? t : 2 * t + i; };
     // S_i = Q_(tile of i) K(kv)^T
     auto issue_s = [&](int i, int t) -> bool {
@@ -461,8 +476,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return true;
     };
-    for (int i = 0; i < 2 && ok; ++i)
-      if (ntask[i] > 0) ok = issue_s(i, 0);
+    for (int i = 0; i < 2 && ok; ++i) {
+      if (i == 0 || two) ok = __all_sync(0xffffffffu, mbar_wait(&bars->q_full[i], 0, abort));
+      if (ok && ntask[i] > 0) ok = issue_s(i, 0);
+    }
     const int nt = max(ntask[0], ntask[1]);
     for (int t = 0; t < nt && ok; ++t)
       for (int i = 0; i < 2 && ok; ++i) {

@@ -41,39 +41,40 @@ struct PlainDivision {
 // Keys that the query at position p of a sequence of L keys sees. All three
 // ends grow with p, so the keys of a run of rows lie in [0, s of the last row)
 // and [lo of the first, hi of the last).
-// Positions and counts are below 2^31; only the products by the frame need
-// more, and divisions stay in 32 bits. by_frame divides by the frame.
+// Positions, counts and frames are below 2^31. So is a frame's first position up to that
+// of the query, and the end of its frame is below 2^32; only the products of sinks and of
+// the window behind the query by the frame need more. by_frame divides by the frame.
 template <class Division>
-__host__ __device__ inline Range visible_range(const sparsepr_visibility& see, long long p,
-                                               long long L, const Division& by_frame) {
+__host__ __device__ inline Range visible_range(const sparsepr_visibility& see, long long pos,
+                                               int L, const Division& by_frame) {
   Range r = {0, 0, 0};
-  if (p < 0 || L <= 0) return r;
+  if (pos < 0 || L <= 0) return r;
+  const uint32_t p = static_cast<uint32_t>(pos), len = static_cast<uint32_t>(L);
   if (see.window == 0 && see.frame == 1) {  // every key, or every key up to its own
-    r.hi = static_cast<int>(see.causal && p + 1 < L ? p + 1 : L);
+    r.hi = static_cast<int>(see.causal && p + 1 < len ? p + 1 : len);
     return r;
   }
-  const long long F = see.frame;
-  const long long f = see.frame == 1 ? p : by_frame.div(static_cast<int>(p));
-  long long end = L;  // keys a causal query may look at
-  if (see.causal && (f + 1) * F < L) end = (f + 1) * F;
-  long long s = see.sinks * F;
-  if (s > end) s = end;
-  long long lo = 0, hi = end;
-  if (see.window > 0) {
-    lo = (f - see.window + 1) * F;
-    if (lo < 0) lo = 0;
-    if (!see.causal && (f + see.window) * F < L) hi = (f + see.window) * F;
+  const uint32_t F = static_cast<uint32_t>(see.frame), W = static_cast<uint32_t>(see.window);
+  const uint32_t next = (F == 1 ? p : static_cast<uint32_t>(by_frame.div(static_cast<int>(p)))) + 1;
+  uint32_t end = len;  // keys a causal query may look at
+  if (see.causal && next * F < len) end = next * F;
+  const uint64_t sink = static_cast<uint64_t>(static_cast<uint32_t>(see.sinks)) * F;
+  const uint32_t s = sink < end ? static_cast<uint32_t>(sink) : end;
+  uint32_t lo = 0, hi = end;
+  if (W > 0) {
+    if (next > W) lo = (next - W) * F;
+    const uint64_t behind = static_cast<uint64_t>(next - 1 + W) * F;
+    if (!see.causal && behind < len) hi = static_cast<uint32_t>(behind);
   }
   if (lo < s) lo = s;
   if (hi < lo) hi = lo;
   r.s = static_cast<int>(s);
-  r.lo = static_cast<int>(lo < L ? lo : L);
+  r.lo = static_cast<int>(lo < len ? lo : len);
   r.hi = static_cast<int>(hi);
-  if (r.hi < r.lo) r.hi = r.lo;
   return r;
 }
 __host__ __device__ inline Range visible_range(const sparsepr_visibility& see, long long p,
-                                               long long L) {
+                                               int L) {
   return visible_range(see, p, L, PlainDivision{see.frame});
 }
 

@@ -677,6 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int c = 0; c < 2 * kHalf; ++c) {
         if (!two && c / kHalf != i) continue;
+
         uint32_t o[32];
         tmem_ld32(o_base + (two ? i * HD : 0) + c * 32, o);
         tmem_wait_ld();

@@ -17,9 +17,9 @@
 // in tensor memory.
 //
 // Bound by the tensor cores with their shared-memory operands: 480p clip (12 heads,
-// 32,760 rows, 9,360 keys each at most) 1.55 to 1.72 ms, 1,020 to 1,130 TFLOP/s of
-// visible pairs, 58% of the tensor cycles at the 1.7 GHz that the power limit leaves;
-// 1.35 ms with no softmax at all, 1.50 ms without the copies of K and V. Tiles of
+// 32,760 rows, 9,360 keys each at most) 1.51 to 1.70 ms, 1,030 to 1,160 TFLOP/s of
+// visible pairs, 60% of the tensor cycles at the 1.7 GHz that the power limit leaves;
+// 1.35 ms with no softmax at all, 1.50 ms without the copies of K and V (of 1.55). Tiles of
 // 128 x 128, because a product with 64 columns takes as long as one with 128.
 #include <type_traits>
 
@@ -900,8 +900,8 @@ cudaError_t launch_hd(const WindowKernelParams& p, const WindowMaps& maps, int u
 //     last one as long as a full one. A key tile costs 1 for 256 rows and 0.6 for 128
 //     (measured 1.7 us and 1.0 us), a block 4 beside its tiles, partial results what
 //     their bytes take at 6.5 TB/s, and the combine kernel 2. (A frame of 1,560 rows and
-//     12 heads against 21,840 keys: 156 units of 128 rows are two rounds, 371 us; 84 of 256
-//     rows in 5 splits three rounds of a fifth, 279 us.)
+//     12 heads against 21,840 keys: 156 units of 128 rows are two rounds, 357 us; 84 of 256
+//     rows in 5 splits three rounds of a fifth, 221 us.)
 WindowPlan window_plan(int B, int Hq, int Hkv, int Nq, int Nk, const sparsepr_visibility& see) {
   WindowPlan w = {};
   const int group = Hq / Hkv;

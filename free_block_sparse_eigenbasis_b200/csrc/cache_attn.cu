@@ -1187,13 +1187,8 @@ cudaError_t launch_cache_attention(const CacheAttnArgs& a, cudaStream_t st) {
   p.units_seq = a.cache.p.Hkv * w.row_tiles;
   p.sub_rows = min(a.cache.p.page, tile_keys(a.cache.p.d));
   // tiles that a sequence can have at most: of its table row, or of what is visible
-  const sparsepr_visibility& see = a.see;
-  long long keys = static_cast<long long>(a.cache.p.max_pages) * a.cache.p.page;
-  if (see.window > 0) {
-    const long long F = see.frame;
-    const long long span = (see.sinks + (see.causal ? 1ll : 2ll) * see.window + 1) * F + a.Nq;
-    if (span < keys) keys = span;
-  }
+  const long long keys =
+      most_visible(a.see, a.Nq, static_cast<long long>(a.cache.p.max_pages) * a.cache.p.page);
   // (a window may begin and the sinks may end inside a tile)
   p.always_whole = keys / tile_keys(a.cache.p.d) + 4 <= kWholeTiles;
   p.combine_rows = 1;

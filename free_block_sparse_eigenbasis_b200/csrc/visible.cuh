@@ -78,6 +78,16 @@ __host__ __device__ inline Range visible_range(const sparsepr_visibility& see, l
   return visible_range(see, p, L, PlainDivision{see.frame});
 }
 
+// Of `keys` keys, how many a run of `rows` rows can need at most. (The product of frames
+// is formed only where it is at most `keys`.)
+inline long long most_visible(const sparsepr_visibility& see, long long rows, long long keys) {
+  if (see.window == 0) return keys;
+  const long long frames = see.sinks + (see.causal ? 1ll : 2ll) * see.window + 1;
+  if (frames > keys / see.frame) return keys;
+  const long long span = frames * see.frame + rows;
+  return span < keys ? span : keys;
+}
+
 // In-use rows of one sequence, clamped to what the buffers hold.
 __device__ __forceinline__ int clamp_count(const int32_t* n, int b, int cap, int otherwise,
                                            DeviceStats* stats, bool report) {

@@ -912,12 +912,7 @@ WindowPlan window_plan(int B, int Hq, int Hkv, int Nq, int Nk, const sparsepr_vi
   for (int rows = 2 * kTileM; rows >= kTileM; rows -= kTileM) {
     if (rows > kTileM && w.R <= kTileM) continue;
     const long long tiles = (w.R + rows - 1) / rows, units = tiles * w.segs;
-    long long keys = Nk;
-    if (see.window > 0) {
-      const long long F = see.frame;
-      const long long span = (see.sinks + (see.causal ? 1ll : 2ll) * see.window + 1) * F + rows;
-      if (span < keys) keys = span;
-    }
+    const long long keys = most_visible(see, rows, Nk);
     const long long key_tiles = (keys + kTileN - 1) / kTileN;
     const double tile_cost = rows > kTileM ? 1.0 : 0.6;
     const auto rounds = [&](long long blocks, long long part) {

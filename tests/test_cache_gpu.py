@@ -567,3 +567,14 @@ def test_cache_agrees_with_the_windowed_attention():
     tol, _ = U.bounds(ref, q.dtype, 64, U.HALF[torch.bfloat16], 0.0, 0.0)
     for o in outs:  # the cached tokens are exactly bf16 values
         assert (np.abs(U.f64(o[0]) - ref["out"]) <= tol).all()
+
+
+@pytest.mark.parametrize("see", [
+    dict(frame=2 ** 31 - 1, window=2 ** 31 - 1, sinks=2 ** 31 - 1, causal=0),
+    dict(frame=2 ** 31 - 1, window=1, sinks=0, causal=1),
+    dict(frame=2, window=2 ** 31 - 1, sinks=1, causal=1)])
+@pytest.mark.parametrize("Nq", [1, 5, 40])
+def test_largest_frames_windows_and_sinks(see, Nq):
+    r = Run(cache_params(2, 1, 64, 16, 90, 40), 19)
+    r.grow([600, 130])
+    assert r.attend(dict(Hq=2, Nq=Nq, **see)) == 0

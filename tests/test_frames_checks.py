@@ -213,3 +213,16 @@ def test_host_tensors_are_refused():
 
 def test_status_string_of_capacity():
     assert "page" in S.status_string(S.ERR_CAPACITY)
+
+
+@pytest.mark.parametrize("causal", [0, 1])
+@pytest.mark.parametrize("big", [dict(frame=2 ** 31 - 1, window=2 ** 31 - 1, sinks=2 ** 31 - 1),
+                                 dict(frame=1 << 20, window=2 ** 31 - 1),
+                                 dict(frame=2 ** 31 - 1, window=1)])
+def test_workspace_of_the_largest_windows(big, causal):
+    """A window that reaches every key needs the scratch of none: products of
+    frames and windows do not overflow where the key ranges are planned."""
+    p = dict(B=1, Hq=12, Hkv=12, Nq=1, Nk=4001, d=128, frame=1, window=0, sinks=0, causal=causal)
+    need = [S.lib.sparsepr_window_workspace_bytes(
+        ctypes.byref(S.make_window_params(dict(p, **kw))), S.BF16) for kw in ({}, big)]
+    assert need[0] == need[1] > 0

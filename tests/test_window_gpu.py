@@ -251,3 +251,31 @@ def test_same_as_the_dense_kernel_without_a_window():
     out, _, _ = call(p, q[None], k[None], v[None])
     # both round their weights to bf16 and the output here once more
     assert (out[0].double() - dense.double()).abs().max() <= 4 * 2.0 ** -8
+
+
+@pytest.mark.parametrize("see_", [
+    dict(frame=2 ** 31 - 1, window=2 ** 31 - 1, sinks=2 ** 31 - 1, causal=0),
+    dict(frame=2 ** 31 - 1, window=1, causal=1), dict(frame=2 ** 30, window=2 ** 31 - 1, causal=1),
+    dict(frame=1, window=2 ** 31 - 1, sinks=2 ** 31 - 1, causal=1),
+    dict(frame=3, window=2 ** 31 - 1, causal=0)])
+def test_largest_frames_windows_and_sinks(see_):
+    p = params(1, 6, 2, 150, 420, 64, **see_)
+    q, k, v = inputs(p, torch.bfloat16, 31)
+    out, lse, status = call(p, q, k, v)
+    assert status == 0
+    verify(p, q, k, v, out, lse)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("sizes", [(3, 21, 7, 37, 301), (2, 10, 2, 131, 517), (1, 13, 13, 257, 259),
+                                   (5, 6, 3, 43, 1025)])
+def test_sizes_that_divide_nothing(sizes, dtype):
+    """Rows, heads, groups, frames and splits that no power of two divides."""
+    for d, frame, window, sinks, causal in ((128, 7, 5, 3, 1), (64, 11, 3, 0, 0), (64, 1, 0, 0, 1)):
+        p = params(*sizes, d, frame, window, sinks, causal)
+        q, k, v = inputs(p, dtype, 77)
+        B, Nq, Nk = p["B"], p["Nq"], p["Nk"]
+        n_q, n_k = [Nq - 3 * b for b in range(B)], [Nk - 101 * b for b in range(B)]
+        out, lse, status = call(p, q, k, v, n_q, n_k)
+        assert status == 0
+        verify(p, q, k, v, out, lse, n_q, n_k, what=(d, frame))

@@ -911,7 +911,7 @@ WindowPlan window_plan(int B, int Hq, int Hkv, int Nq, int Nk, const sparsepr_vi
   double best = -1.0;
   for (int rows = 2 * kTileM; rows >= kTileM; rows -= kTileM) {
     if (rows > kTileM && w.R <= kTileM) continue;
-    const long long tiles = (w.R + rows - 1) / rows, units = tiles * w.segs;
+    const long long tiles = (static_cast<long long>(w.R) + rows - 1) / rows, units = tiles * w.segs;
     const long long keys = most_visible(see, rows, Nk);
     const long long key_tiles = (keys + kTileN - 1) / kTileN;
     const double tile_cost = rows > kTileM ? 1.0 : 0.6;

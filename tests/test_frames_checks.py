@@ -226,3 +226,11 @@ def test_workspace_of_the_largest_windows(big, causal):
     need = [S.lib.sparsepr_window_workspace_bytes(
         ctypes.byref(S.make_window_params(dict(p, **kw))), S.BF16) for kw in ({}, big)]
     assert need[0] == need[1] > 0
+
+
+def test_workspace_of_the_longest_run_of_queries():
+    """Units are counted without overflow up to the last row count allowed: the
+    scratch is at most that of 16 rounds of cut units of 256 rows."""
+    p = dict(B=1, Hq=1, Hkv=1, Nq=2 ** 31 - 1, Nk=64, d=64, frame=1, window=0, sinks=0, causal=1)
+    need = S.lib.sparsepr_window_workspace_bytes(ctypes.byref(S.make_window_params(p)), S.BF16)
+    assert 0 < need <= 16 * 148 * 256 * (64 + 1) * 4 + 4096

@@ -233,10 +233,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   using L = Smem<HD>;
   constexpr int kAtoms = HD / 64;
   const WindowArgs& a = p.a;
-  // the combine kernel, if there is one, may be put in place; it waits for all blocks
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x >= 8 * 32 && threadIdx.x < 8 * 32 + 3)
     prefetch_map(threadIdx.x == 8 * 32 ? &maps.q : threadIdx.x == 8 * 32 + 1 ? &maps.k : &maps.v);
+  // Put in place beside the tail of what came before on the stream, all of which is
+  // waited for here, before anything is read. (One token 13.9 to 13.6 us, the ragged
+  // prompts 20.1 to 19.7.) The combine kernel, if there is one, is put in place likewise.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // block = (unit, split)
   const bool partial = static_cast<int>(blockIdx.x) >= p.whole && p.splits > 1;
   const int splits = partial ? p.splits : 1;
@@ -871,10 +874,19 @@ cudaError_t launch_hd(const WindowKernelParams& p, const WindowMaps& maps, int u
   if (e != cudaSuccess) return e;
   const unsigned blocks = static_cast<unsigned>(p.whole) +
                           static_cast<unsigned>(units - p.whole) * p.splits;
-  window_attn_kernel<HD, T><<<blocks, kThreads, kSmemBytes, st>>>(maps, p);
-  e = cudaGetLastError();
+  cudaLaunchConfig_t first = {};  // programmatic dependent launch
+  first.gridDim = dim3(blocks);
+  first.blockDim = dim3(kThreads);
+  first.dynamicSmemBytes = kSmemBytes;
+  first.stream = st;
+  cudaLaunchAttribute early[1];
+  early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early[0].val.programmaticStreamSerializationAllowed = 1;
+  first.attrs = early;
+  first.numAttrs = 1;
+  e = cudaLaunchKernelEx(&first, window_attn_kernel<HD, T>, maps, p);
   if (e != cudaSuccess || p.whole == units) return e;
-  // launched beside the tail of the attention kernel (programmatic dependent launch)
+  // launched beside the tail of the attention kernel
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((min(p.unit_rows, p.R) + 7) / 8, units - p.whole);
   cfg.blockDim = dim3(256);

@@ -279,3 +279,51 @@ def test_sizes_that_divide_nothing(sizes, dtype):
         out, lse, status = call(p, q, k, v, n_q, n_k)
         assert status == 0
         verify(p, q, k, v, out, lse, n_q, n_k, what=(d, frame))
+
+
+@pytest.mark.parametrize("splits", [False, True])
+def test_behind_copies_and_other_streams(splits):
+    """The inputs are the results of copies, fills and of another stream's work
+    right before the call, eagerly and in a captured graph; calls that depend on
+    one another follow without a pause."""
+    # one unit of many keys is cut, many units are not
+    p = params(1, 2, 2, 3, 5000, 128) if splits else params(2, 40, 40, 300, 400, 128, window=64)
+    q, k, v = inputs(p, torch.bfloat16, 41)
+    k2, v2 = k.flip(2).contiguous(), v.flip(2).contiguous()
+    first, _, _ = call(p, q, k, v)
+    want, want_lse, _ = call(p, first, k2, v2)
+    side = torch.cuda.Stream()
+    sq, sk, sv, mid, out = (torch.zeros_like(t) for t in (q, k, v, q, q))
+    lse = torch.zeros(q.shape[:3], device="cuda")
+    ws = S.allocate_window_workspace(p, q.dtype)
+
+    def step():
+        out.zero_()
+        sk.copy_(k)
+        sv.copy_(v)
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            sq.copy_(q)
+        here.wait_stream(side)
+        S.sparsepr_window_attention(sq, sk, sv, p, mid, ws)
+        sk.copy_(k2)
+        sv.fill_(0)
+        sv.copy_(v2)
+        S.sparsepr_window_attention(mid, sk, sv, p, out, ws, lse=lse)  # the same workspace
+        S.sparsepr_window_attention(mid, sk, sv, p, out, ws, lse=lse)
+
+    for _ in range(5):
+        step()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for _ in range(5):
+        for t in (sq, sk, sv, mid, out, lse):
+            t.fill_(5)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    assert U.status(ws) == 0

@@ -274,7 +274,9 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
   LiteralScratch<kDecodeThreads>& scratch =
       *reinterpret_cast<LiteralScratch<kDecodeThreads>*>(smem + L::merge_off);
 
-  // the combine kernel may be put in place as blocks end; it waits for all of them
+  // Put in place beside the tail of what came before on the stream, all of which is
+  // waited for here; the combine kernel is put in place likewise as blocks end.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == 0) {
     for (int s = 0; s < L::kStages; ++s) mbar_init(&ms.full[0][0] + s, 1);
@@ -1083,10 +1085,19 @@ cudaError_t launch_decode(const DecodeParams& p, const DecodeMaps& maps, cudaStr
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(cache_decode_kernel<HD, NT, T>), kBytes,
                              allowed);
   if (e != cudaSuccess) return e;
-  cache_decode_kernel<HD, NT, T><<<kDecodeBlocks, kDecodeThreads, kBytes, st>>>(maps, p);
-  e = cudaGetLastError();
+  cudaLaunchConfig_t first = {};  // programmatic dependent launch
+  first.gridDim = dim3(kDecodeBlocks);
+  first.blockDim = dim3(kDecodeThreads);
+  first.dynamicSmemBytes = kBytes;
+  first.stream = st;
+  cudaLaunchAttribute early[1];
+  early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early[0].val.programmaticStreamSerializationAllowed = 1;
+  first.attrs = early;
+  first.numAttrs = 1;
+  e = cudaLaunchKernelEx(&first, cache_decode_kernel<HD, NT, T>, maps, p);
   if (e != cudaSuccess || p.always_whole) return e;
-  // launched beside the tail of the decode kernel (programmatic dependent launch)
+  // launched beside the tail of the decode kernel
   cudaLaunchConfig_t cfg = {};
   const int rows = min(p.rows, p.R);
   cfg.gridDim = dim3(p.a.cache.p.B * p.units_seq, (rows + p.combine_rows - 1) / p.combine_rows);

@@ -5,10 +5,13 @@
 //   x_ij = (scale log2(e) ks_j) q_i . k8_j,
 //   out_i = sum_j 2^(x_ij + log2 vs_j - M_i) v8_j * 2^(M_i - m_i) / l_i,
 //   l_i = sum_j 2^(x_ij - m_i),
-// m_i = max_j x_ij, M_i = max_j (x_ij + log2 vs_j). With M as the reference of the
-// second product its weights are at most 1 whatever the scales are, so they
-// fit fp16 (11 bits), and so do all e4m3 values, exactly: both products are
-// fp16 MMAs with fp32 sums.
+// m_i near max_j x_ij, M_i near max_j (x_ij + log2 vs_j). With M as the reference of the
+// second product its weights are below 2^16 whatever the scales are, so they
+// fit fp16, and so do all e4m3 values, exactly: both products are fp16 MMAs with fp32
+// sums. fp16 holds 11 bits of a weight down to 2^-14 and nothing below 2^-25, and keys that
+// far below the largest can still be all of the output, where the values of the largest are
+// 0: what fp16 leaves of a tile with such weights is added by a product in tf32, which
+// reaches down to 2^-126.
 //
 // Two kernels. Few query rows per key head (one token, a few speculated
 // ones): the cache is read once and the call is bound by that; see
@@ -191,6 +194,21 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       "{%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// D (16x8, fp32) += A (16x8, tf32) B (8x8, tf32)
+__device__ __forceinline__ void mma1688_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                             uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// rounded to tf32: 11 significant bits
+__device__ __forceinline__ uint32_t to_tf32(float x) {
+  uint32_t r;
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
+  return r;
 }
 
 // transpose of an 8x8 matrix of 16-bit values (lane 4 r + c holds row r, columns 2c, 2c + 1)
@@ -639,9 +657,10 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
 #pragma unroll
         for (int kt = 1; kt < kKt; ++kt) one_scale = one_scale && lv[kt] == lv[0];
         const bool plain = whole && k0 >= from && k0 + kTile <= to;  // the same in the whole warp
-        // The references m and M of a row (-inf: nothing seen) are maxima of an earlier
-        // tile; they move only when a value passes them by 2^60 (weights of l, fp32)
-        // or 2^12 (weights of the second product, fp16 up to 2^16).
+        // The references m and M of a row (-inf: nothing seen) come from the maxima of an
+        // earlier tile; they move only when a value passes them by 2^60 (weights of l, fp32)
+        // or 2^15 (weights of the second product, fp16 up to 2^16). M is set 8 below the
+        // maximum, so that weights 22 to 29 below the largest are still normal fp16 numbers.
         float tm[NT][2], tM[NT][2];  // this lane's maxima
         bool rise = false;
 #pragma unroll
@@ -666,7 +685,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
               }
             if (one_scale) tM[nt][e] = tm[nt][e] + lv[0];
             if (plain) seen[nt][e] = true;
-            rise = rise || tm[nt][e] > m[nt][e] + 60.f || tM[nt][e] > M[nt][e] + 12.f;
+            rise = rise || tm[nt][e] > m[nt][e] + 60.f || tM[nt][e] > M[nt][e] + 15.f;
           }
         if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
@@ -680,7 +699,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
                 y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, w));
               }
               x = fmaxf(m[nt][e], x);
-              y = fmaxf(M[nt][e], y);
+              y = fmaxf(M[nt][e], y - 8.f);
               // -inf only where nothing has been seen: the sums are 0 then
               l[nt][e] *= x == -INFINITY ? 0.f : ex2_approx(m[nt][e] - x);
               af[nt][e] = y == -INFINITY ? 0.f : ex2_approx(M[nt][e] - y);
@@ -703,6 +722,30 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
             nM[nt][e] = M[nt][e] == -INFINITY ? 0.f : M[nt][e];
           }
         // ---- weights and the second product, 16 keys at a time ----
+        constexpr int kW = HD / 32;  // words of a value per lane
+        // HD / 8 bytes of the value of a key of the tile
+        auto load_value = [&](int key, bool unread, uint32_t (&vw)[kW]) {
+          if (HD == 128) {
+            const uint4 v = *reinterpret_cast<const uint4*>(vs8 + key * HD + (g ^ (key & 7)) * 16);
+            vw[0] = v.x;
+            vw[1] = v.y;
+            vw[kW - 2] = v.z;
+            vw[kW - 1] = v.w;
+          } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(
+                vs8 + key * HD + ((g >> 1) ^ ((key >> 1) & 3)) * 16 + (g & 1) * 8);
+            vw[0] = v.x;
+            vw[1] = v.y;
+          }
+          if (!plain) {
+            // a value that no row sees may be anything, also NaN
+            const int kx = k0 + key;
+            if (unread || !(kx < s.SA || (kx >= s.LB && kx < s.HB)))
+#pragma unroll
+              for (int w = 0; w < kW; ++w) vw[w] = 0u;
+          }
+        };
+        __half2 least = __float2half2_rn(1.f);  // of the weights of visible keys
 #pragma unroll
         for (int kt = 0; kt < kKt; ++kt) {
           uint32_t pb[NT][2];
@@ -714,34 +757,17 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
               const float v0 = acc[kt][nt][2 * x], v1 = acc[kt][nt][2 * x + 1];
               l[nt][0] += ex2_approx(v0 - nm[nt][0]);
               l[nt][1] += ex2_approx(v1 - nm[nt][1]);
-              pb[nt][x] = transpose8x8(pack_f16x2(ex2_approx(v0 + sh[0]), ex2_approx(v1 + sh[1])));
+              const uint32_t p2 = pack_f16x2(ex2_approx(v0 + sh[0]), ex2_approx(v1 + sh[1]));
+              uint32_t p2_seen = p2;
+              if (!plain) p2_seen |= (v0 == -INFINITY ? 0x3c00u : 0u) | (v1 == -INFINITY ? 0x3c000000u : 0u);
+              least = __hmin2(least, *reinterpret_cast<const __half2*>(&p2_seen));
+              pb[nt][x] = transpose8x8(p2);
             }
           }
-          constexpr int kW = HD / 32;  // words of a value per lane
-          uint32_t vw[4][kW];          // keys 2t, 2t+1, 2t+8, 2t+9: HD / 8 bytes of each
+          uint32_t vw[4][kW];  // keys 2t, 2t+1, 2t+8, 2t+9
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int key = kt * 16 + 2 * t4 + (e & 1) + (e >> 1) * 8;
-            if (HD == 128) {
-              const uint4 v = *reinterpret_cast<const uint4*>(vs8 + key * HD + (g ^ (key & 7)) * 16);
-              vw[e][0] = v.x;
-              vw[e][1] = v.y;
-              vw[e][kW - 2] = v.z;
-              vw[e][kW - 1] = v.w;
-            } else {
-              const uint2 v = *reinterpret_cast<const uint2*>(
-                  vs8 + key * HD + ((g >> 1) ^ ((key >> 1) & 3)) * 16 + (g & 1) * 8);
-              vw[e][0] = v.x;
-              vw[e][1] = v.y;
-            }
-            if (!plain) {
-              // a value that no row sees may be anything, also NaN
-              const int kx = k0 + key;
-              if (!(ks[kt] >= 0.f) || !(kx < s.SA || (kx >= s.LB && kx < s.HB)))
-#pragma unroll
-                for (int w = 0; w < kW; ++w) vw[e][w] = 0u;
-            }
-          }
+          for (int e = 0; e < 4; ++e)
+            load_value(kt * 16 + 2 * t4 + (e & 1) + (e >> 1) * 8, !(ks[kt] >= 0.f), vw[e]);
 #pragma unroll
           for (int w = 0; w < kW; ++w) {
 #pragma unroll
@@ -754,6 +780,53 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
               for (int nt = 0; nt < NT; ++nt) mma16816(o[2 * w + x][nt], va, pb[nt][0], pb[nt][1]);
             }
           }
+        }
+        // ---- weights below the normal fp16 numbers: what fp16 left of them, in tf32 ----
+        // (By way of shared memory and in a loop of its own: with the products in registers in
+        // place of those above the calls that never come here took 1% to 8% longer, not up to 1%.)
+        const uint32_t lw = *reinterpret_cast<const uint32_t*>(&least);
+        if (__any_sync(0xffffffffu, (lw & 0x7c00u) == 0u || (lw & 0x7c000000u) == 0u)) {
+          // [key][row], in place of the keys, which have been read
+          float* const left = reinterpret_cast<float*>(my_stages + st * L::kStageBytes);
+          uint32_t unread = 0;  // groups of 16 keys that were not fetched
+          __syncwarp();
+#pragma unroll
+          for (int kt = 0; kt < kKt; ++kt) {
+            unread |= ks[kt] >= 0.f ? 0u : 1u << kt;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float w = ex2_approx(acc[kt][nt][e] + (lv[kt] - nM[nt][e & 1]));
+                left[(kt * 16 + (e >> 1) * 8 + g) * kRows + 8 * nt + 2 * t4 + (e & 1)] =
+                    w - __half2float(__float2half_rn(w));
+              }
+          }
+          __syncwarp();
+#pragma unroll 1
+          for (int j = 0; j < kTile / 8; ++j) {  // 8 keys: 2t and 2t + 1 are rows t and t + 4 of the operand
+            const int key = j * 8 + 2 * t4;
+            uint32_t vw[2][kW];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) load_value(key + e, (unread >> (j >> 1)) & 1u, vw[e]);
+            uint32_t p2[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) p2[nt][e] = to_tf32(left[(key + e) * kRows + 8 * nt + g]);
+#pragma unroll
+            for (int mt = 0; mt < kSteps; ++mt) {
+              const uint32_t v = __byte_perm(vw[0][mt / 2], vw[1][mt / 2], mt & 1 ? 0x7362 : 0x5140);
+              const uint32_t v0 = e4m3x2_to_f16x2(v), v1 = e4m3x2_to_f16x2(v >> 16);
+              const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&v0));
+              const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&v1));
+              const uint32_t va[4] = {__float_as_uint(f0.x), __float_as_uint(f1.x),
+                                      __float_as_uint(f0.y), __float_as_uint(f1.y)};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma1688_tf32(o[mt][nt], va, p2[nt][0], p2[nt][1]);
+            }
+          }
+          fence_proxy_async_smem();  // the next copy into this stage comes after these writes
         }
         __syncwarp();
         if (kth + kDepth < count) fetch(kth + kDepth);

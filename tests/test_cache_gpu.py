@@ -578,3 +578,39 @@ def test_largest_frames_windows_and_sinks(see, Nq):
     r = Run(cache_params(2, 1, 64, 16, 90, 40), 19)
     r.grow([600, 130])
     assert r.attend(dict(Hq=2, Nq=Nq, **see)) == 0
+
+
+@pytest.mark.parametrize("at", [0, 690])
+@pytest.mark.parametrize("ratio,page", [(1, 64), (2.0 ** 6, 64), (2.0 ** 10, 16)])
+@pytest.mark.parametrize("gap", [16, 20, 25, 30, 60])
+@pytest.mark.parametrize("rows", [1, 8, 32])
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_strong_key_without_a_value(d, rows, gap, ratio, page, at):
+    """A key whose logit lies `gap` log2 units above all others and whose value is 0, in a
+    page whose value scale is `ratio` times the others': the output is the other keys',
+    whose weights are that much smaller than the largest. The queries are bf16 values, which
+    the call takes as they are; the output is fp32, so that the weights' 11 bits show."""
+    L, scale = 700, 0.125
+    Hq, Nq = {1: (1, 1), 8: (8, 1), 32: (4, 8)}[rows]
+    p = cache_params(1, 1, d, page, 50, 48)
+    r = Run(p)
+    assert r.reserve([L])
+    k = U.normal((1, 1, L, d), 1, scale=0.25)
+    v = U.normal((1, 1, L, d), 2, scale=0.25) + 1
+    k[..., 0], k[0, 0, at, 0] = 0.0, 16.0
+    v[0, 0, at] = 0
+    v[0, 0, at ^ 1, 0] = 2.0 * ratio
+    S.sparsepr_cache_append(k, v, p, r.c, r.start, None, r.ws)
+    r.m.append(U.f64(k), U.f64(v), [0], [L])
+    r.same()
+    q = U.normal((1, Hq, Nq, d), 3, scale=0.25).float()
+    q[..., 0] = gap / (scale * 16 * 1.4426950408889634)
+    q = q.bfloat16().float()
+    attn = dict(Hq=Hq, Nq=Nq, scale=scale)
+    out, lse = torch.zeros_like(q), torch.zeros(q.shape[:3], device="cuda")
+    ws = S.allocate_cache_workspace(p, attn)
+    S.sparsepr_cache_attention(q, p, r.c, attn, out, ws, lse=lse)
+    ref = F.attention(U.f64(q[0]), r.m.tokens(0, "k"), r.m.tokens(0, "v"), Nq,
+                      dict(frame=1, window=0, sinks=0, causal=1), scale)
+    U.check(out[0], lse[0], ref, torch.float32, d, F16)
+    assert U.status(ws) == 0

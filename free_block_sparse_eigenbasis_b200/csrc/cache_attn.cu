@@ -494,9 +494,9 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
     const BlockSync sync;
     uint32_t taken = 0;  // tiles of this warp so far
     // Queries of a run as the first product's operand, in the merge buffer, which is
-    // free then: lane (g, t) holds row g + 8 nt, in fp16, scaled by a power of two to less
-    // than 2 in magnitude (exact for bf16 values unless they lie 2^14 below the
-    // row's largest). Thread = (row, 1 / 8 of its columns).
+    // free then: lane (g, t) holds row g + 8 nt, in fp16, scaled by a power of two so that the
+    // row's largest value lies in [2^14, 2^15): values down to 2^-28 of it keep 11 bits (and
+    // bf16 values, of 8 bits, are exact down to 2^-31 of it). Thread = (row, 1 / 8 of its columns).
     uint2* const qs = reinterpret_cast<uint2*>(merge);  // [NT][kSteps][32]
     auto put_queries = [&](const Run& r, const SeqTiles<HD>& s, int h) {
       constexpr int kC = HD / 8;  // 16 or 8 columns a thread: a chunk, or half of one
@@ -527,8 +527,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
 #pragma unroll
         for (int w = 1; w < 8; w <<= 1) top = fmaxf(top, __shfl_xor_sync(eight, top, w));
         // exponent of the row's largest value, so that its power of two is normal both ways
-        const int ex = top > 0.f ? min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -100), 100) : 0;
-        const float down = __uint_as_float((127 - ex) << 23);
+        const int ex = top > 0.f ? min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -112), 127) : 0;
+        const float down = __uint_as_float((127 + 14 - ex) << 23);
         const int nt = rr >> 3, to = (rr & 7) * 4;
 #pragma unroll
         for (int k = 0; k < kC; k += 4) {
@@ -546,7 +546,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
           ms.range[rr] = rg;
           ms.live[rr] = on;
           ms.valid[rr] = have;
-          ms.q_scale[rr] = a.sc * __uint_as_float((127 + ex) << 23);
+          ms.q_scale[rr] = a.sc * __uint_as_float((127 - 14 + ex) << 23);
         }
       }
     };

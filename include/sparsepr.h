@@ -532,8 +532,9 @@ sparsepr_status sparsepr_cache_append(const void* k, const void* v, sparsepr_dty
  * values that the pages of each sequence stand for, L = len[b].
  *   q [B, Hq, Nq, d] dtype dt, n_q, out, lse as there.
  * Up to 32 query rows per key head (Hq / Hkv * Nq) the cache is read in place,
- * queries and weights are rounded to 11 significant bits (weights down to 2^-100
- * of a row's largest; below that they may count as 0); beyond that the pages
+ * queries and weights are rounded to 11 significant bits (queries down to 2^-28 of a
+ * row's largest, below that to multiples of 2^-39 of it; weights down to 2^-100 of a
+ * row's largest, below that they may count as 0); beyond that the pages
  * are widened to bf16 in ws first and queries and weights are rounded to bf16 (8
  * bits), as in sparsepr_window_attention. The softmax and all sums are fp32.
  * A token whose table entry holds no page raises SPARSEPR_ERR_INVALID_ARG and

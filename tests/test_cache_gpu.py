@@ -614,3 +614,34 @@ def test_a_strong_key_without_a_value(d, rows, gap, ratio, page, at):
                       dict(frame=1, window=0, sinks=0, causal=1), scale)
     U.check(out[0], lse[0], ref, torch.float32, d, F16)
     assert U.status(ws) == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("Nq", [1, 3])
+@pytest.mark.parametrize("big", [2.0 ** 14, 2.0 ** 20, 2.0 ** 28, 2.0 ** 110])
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_query_channel_far_above_the_others(d, big, Nq, dtype):
+    """One large channel of the queries meets zeros of the keys: the logits are the other
+    channels'. The queries are bf16 values that the call can take as they are: multiples of
+    2^-39 of the large one (at 2^28 they are rounded to that here)."""
+    p = cache_params(1, 1, d, 16, 20, 16)
+    r = Run(p, 7)
+    assert r.reserve([200])
+    k, v = U.normal((1, 1, 200, d), 1), U.normal((1, 1, 200, d), 2)
+    k[..., 0] = 0
+    S.sparsepr_cache_append(k, v, p, r.c, r.start, None, r.ws)
+    r.m.append(U.f64(k), U.f64(v), [0], [200])
+    q = U.normal((1, 2, Nq, d), 3)
+    if big == 2.0 ** 28:  # multiples of 2^-9
+        q = torch.round(q.float() * 16).div(16).bfloat16()
+    scale = 1.0
+    if big == 2.0 ** 110:
+        q, scale = q * 2.0 ** 100, 2.0 ** -100
+    q = q.to(dtype)
+    q[..., 0] = big
+    attn = dict(Hq=2, Nq=Nq, scale=scale)
+    out, lse = torch.zeros_like(q), torch.zeros(q.shape[:3], device="cuda")
+    S.sparsepr_cache_attention(q, p, r.c, attn, out, S.allocate_cache_workspace(p, attn), lse=lse)
+    ref = F.attention(U.f64(q[0]), r.m.tokens(0, "k"), r.m.tokens(0, "v"), Nq,
+                      dict(frame=1, window=0, sinks=0, causal=1), scale)
+    U.check(out[0], lse[0], ref, dtype, d, F16)

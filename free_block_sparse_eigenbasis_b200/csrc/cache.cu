@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(kAppendThreads)
     if (first) raise_status(a.stats, SPARSEPR_ERR_INVALID_ARG);
     end = room;
   }
-  if (col * page >= end) return;
+  if (start >= end || col * page >= end) return;  // nothing for this sequence, or not here
   const int id = a.c.table[static_cast<size_t>(b) * a.p.max_pages + col];
   if (!page_ok(a, id) || a.c.ref[id] != 1) {  // no page, or one that other sequences share
     if (threadIdx.x == 0) raise_status(a.stats, SPARSEPR_ERR_INVALID_ARG);

@@ -645,3 +645,21 @@ def test_a_query_channel_far_above_the_others(d, big, Nq, dtype):
     ref = F.attention(U.f64(q[0]), r.m.tokens(0, "k"), r.m.tokens(0, "v"), Nq,
                       dict(frame=1, window=0, sinks=0, causal=1), scale)
     U.check(out[0], lse[0], ref, dtype, d, F16)
+
+
+def test_append_of_nothing_beside_a_shared_page():
+    """Sequences that get no token in this step may share their last, partly filled page, or
+    hold none: nothing is written for them and nothing is wrong."""
+    p = cache_params(4, 1, 64, 16, 12, 4)
+    r = Run(p)
+    r.grow([20, 5, 0, 0])
+    S.sparsepr_cache_fork(U.i32([0]), U.i32([2]), p, r.c, r.ws)
+    r.m.fork([0], [2])
+    r.grow([0, 2, 0, 0], T=3)
+    assert r.status() == 0
+    r.same()
+    # a place inside the table without a page, and the end of the row
+    x = torch.ones(4, 1, 3, 64, dtype=torch.bfloat16, device="cuda")
+    S.sparsepr_cache_append(x, x, p, r.c, U.i32([20, 7, 64, 40]), U.i32([0, 0, 0, 0]), r.ws)
+    assert r.status() == 0
+    r.same()

@@ -653,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // ---------------- epilogue: O / l -> global -------------------------------
     float f0, f1 = 0.f, lsev;  // factors of this thread's O and the other one's, log2-sum-exp
-    bool has1 = false;
+    bool has1 = false, use0 = false, use1 = false;  // one tile: halves that hold keys of the row
     if (two) {
       f0 = live && l_sum > 0.f ? 1.f / l_sum : 0.f;
       lsev = live && l_sum > 0.f ? m_ref + __log2f(l_sum) : -INFINITY;
@@ -671,8 +671,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       has1 = ntask[1] > 0;
       const float mm = has1 ? fmaxf(m0, m1) : m0;
       // a half that holds none of the row's keys has the reference -inf
-      const float a0 = m0 == -INFINITY ? 0.f : ex2_approx(m0 - mm);
-      const float a1 = has1 && m1 != -INFINITY ? ex2_approx(m1 - mm) : 0.f;
+      use0 = m0 != -INFINITY;
+      use1 = has1 && m1 != -INFINITY;
+      const float a0 = use0 ? ex2_approx(m0 - mm) : 0.f;
+      const float a1 = use1 ? ex2_approx(m1 - mm) : 0.f;
       const float l = l0 * a0 + (has1 ? l1 * a1 : 0.f);
       const bool far = mm != -INFINITY && !(fabsf(mm) < kMaxReference);
       const float inv = live && l > 0.f ? 1.f / l : 0.f;
@@ -714,8 +716,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
 #pragma unroll
           for (int k = 0; k < 32; ++k)
-            o[k] = __float_as_uint((f0 > 0.f ? __uint_as_float(o[k]) * f0 : 0.f) +
-                                   (f1 > 0.f ? __uint_as_float(o1[k]) * f1 : 0.f));
+            o[k] = __float_as_uint((use0 ? __uint_as_float(o[k]) * f0 : 0.f) +
+                                   (use1 ? __uint_as_float(o1[k]) * f1 : 0.f));
         }
         const float f = two ? f0 : 1.f;
         float sum = 0.f;  // NaN when a value is not finite
@@ -783,7 +785,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // out = sum_s 2^(l_s - M) O_s / sum_s 2^(l_s - M), M = max_s l_s, over the splits'
 // normalised partial outputs in a fixed order; a split without any of the
-// row's keys has l_s = -inf and weight 0. A warp per row: the lanes take one
+// row's keys has l_s = -inf and is left out (one whose weight is 0 only by underflow is
+// not: it may hold NaN or infinities that the row sees). A warp per row: the lanes take one
 // split's log-sum-exp each, then HD / 32 columns each.
 template <int HD, typename T>
 __global__ void __launch_bounds__(256) window_combine_kernel(const WindowKernelParams p) {
@@ -818,12 +821,13 @@ __global__ void __launch_bounds__(256) window_combine_kernel(const WindowKernelP
 #pragma unroll
   for (int w = 16; w > 0; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
   const bool nan = __any_sync(0xffffffffu, l != l);
+  const uint32_t there = __ballot_sync(0xffffffffu, l != -INFINITY);
   const float weight = l == -INFINITY ? 0.f : exp2f(l - M);
   float num[kC] = {}, den = 0.f;
 #pragma unroll
   for (int s = 0; s < kMaxWindowSplits; ++s) {
     const float w = __shfl_sync(0xffffffffu, weight, s);
-    if (s < p.splits && w != 0.f) {  // a range without a key of the row may not have written its part
+    if ((there >> s) & 1u) {  // a range without a key of the row may not have written its part
       den += w;
 #pragma unroll
       for (int e = 0; e < kC; ++e) num[e] = fmaf(w, part[s].v[e], num[e]);

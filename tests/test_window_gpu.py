@@ -327,3 +327,23 @@ def test_behind_copies_and_other_streams(splits):
         torch.cuda.synchronize()
         assert torch.equal(out, want) and torch.equal(lse, want_lse)
     assert U.status(ws) == 0
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("H,Nk,weak", [(2, 5000, 4000), (2, 256, 128), (296, 256, 128)])
+def test_values_that_are_not_finite_under_vanishing_weights(H, Nk, weak, value):
+    """The first keys lie 512 log2 units below the others, so that whole parts of the sum
+    weigh 0 in fp32 where they are joined; 0 times a NaN or an infinity is NaN there as
+    everywhere, whether the keys are cut into ranges or not."""
+    p = params(1, H, H, 3, Nk, 128, causal=0, scale=1.0)
+    q, k, v = inputs(p, torch.bfloat16, 5, 0.1)
+    q[..., 0], k[..., 0] = 16.0, 0.0
+    k[:, :, :weak, 0] = -22.25
+    ref = F.attention(U.f64(q[0]), U.f64(k[0]), U.f64(v[0]), 3, see(p), 1.0)
+    v[0, :, 10, 5] = value
+    out, lse, st = call(p, q, k, v)
+    assert st == 0
+    assert not torch.isfinite(out[..., 5]).any()
+    keep = [c for c in range(128) if c != 5]
+    U.check(out[0][..., keep], lse[0], dict(ref, out=ref["out"][..., keep], mass=ref["mass"][..., keep]),
+            q.dtype, 128, WEIGHTS)

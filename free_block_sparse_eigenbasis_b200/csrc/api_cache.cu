@@ -26,6 +26,14 @@ sparsepr_status check_see(const sparsepr_visibility& s) {
   return SPARSEPR_OK;
 }
 
+// scale log2(e) as the kernels take it: at least the least normal number, since a masked
+// logit is -inf times it. (Products below 2^100 give logits of 0 there, to fp32's bits.)
+float log2_scale(double scale, int d) {
+  const double s = scale > 0.0 ? scale : 1.0 / sqrt(static_cast<double>(d));
+  return fmaxf(static_cast<float>(s * 1.4426950408889634074), 1.17549435e-38f);
+}
+bool good_scale(double scale) { return scale >= 0.0 && isfinite(log2_scale(scale, 64)); }
+
 // sizes that index arithmetic and launch grids hold
 constexpr long long kMaxRows = (1ll << 31) - 1;
 constexpr long long kMaxHeads = 65535;
@@ -36,7 +44,7 @@ sparsepr_status check_window(const sparsepr_window_params* p) {
   if (p->Nq < 0 || p->Nk < 0) return SPARSEPR_ERR_INVALID_ARG;
   const sparsepr_status s = check_see(p->see);
   if (s != SPARSEPR_OK) return s;
-  if (!(isfinite(p->scale) && p->scale >= 0.0)) return SPARSEPR_ERR_INVALID_ARG;
+  if (!good_scale(p->scale)) return SPARSEPR_ERR_INVALID_ARG;
   if (p->d != 64 && p->d != 128) return SPARSEPR_ERR_UNSUPPORTED;
   const long long bh = static_cast<long long>(p->B) * p->Hq;
   if (bh > kMaxHeads || bh * p->Nq > kMaxRows ||
@@ -63,7 +71,7 @@ sparsepr_status check_cache_attention(const sparsepr_cache_params* p,
   if (!a || a->Hq < 1 || a->Hq % p->Hkv != 0 || a->Nq < 0) return SPARSEPR_ERR_INVALID_ARG;
   s = check_see(a->see);
   if (s != SPARSEPR_OK) return s;
-  if (!(isfinite(a->scale) && a->scale >= 0.0)) return SPARSEPR_ERR_INVALID_ARG;
+  if (!good_scale(a->scale)) return SPARSEPR_ERR_INVALID_ARG;
   const long long bh = static_cast<long long>(p->B) * a->Hq;
   if (bh > kMaxHeads || bh * a->Nq > kMaxRows) return SPARSEPR_ERR_UNSUPPORTED;
   // tiles of all sequences are counted in 32 bits
@@ -95,11 +103,6 @@ int sm_count() {
   if (cudaGetDevice(&dev) == cudaSuccess)
     cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
   return n;
-}
-
-float log2_scale(double scale, int d) {
-  const double s = scale > 0.0 ? scale : 1.0 / sqrt(static_cast<double>(d));
-  return static_cast<float>(s * 1.4426950408889634074);
 }
 
 size_t carve_window(const sparsepr_window_params& p, sparsepr_dtype dt, char* base, WindowArgs* a) {

@@ -436,7 +436,7 @@ typedef struct {
   int32_t Nk;   /* key rows per sequence (0 is allowed) */
   int32_t d;    /* 64 or 128 */
   sparsepr_visibility see;
-  double scale; /* softmax scale; 0 selects 1/sqrt(d) */
+  double scale; /* softmax scale, below 2^127; 0 selects 1/sqrt(d) */
 } sparsepr_window_params;
 
 /* Bytes of workspace of sparsepr_window_attention (0: invalid parameters). */
@@ -489,7 +489,7 @@ typedef struct {
   int32_t Hq;  /* query heads, a multiple of Hkv; B * Hq <= 65535 */
   int32_t Nq;  /* query rows per sequence (0 is allowed) */
   sparsepr_visibility see;
-  double scale; /* softmax scale; 0 selects 1/sqrt(d) */
+  double scale; /* softmax scale, below 2^127; 0 selects 1/sqrt(d) */
 } sparsepr_cache_attention_params;
 
 /* Bytes of workspace of the cache calls; with `a` NULL of all but

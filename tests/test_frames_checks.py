@@ -234,3 +234,14 @@ def test_workspace_of_the_longest_run_of_queries():
     p = dict(B=1, Hq=1, Hkv=1, Nq=2 ** 31 - 1, Nk=64, d=64, frame=1, window=0, sinks=0, causal=1)
     need = S.lib.sparsepr_window_workspace_bytes(ctypes.byref(S.make_window_params(p)), S.BF16)
     assert 0 < need <= 16 * 148 * 256 * (64 + 1) * 4 + 4096
+
+
+@pytest.mark.parametrize("scale,code", [(1e39, S.ERR_INVALID_ARG), (1e300, S.ERR_INVALID_ARG),
+                                        (2.0 ** 126, S.OK), (1e-300, S.OK)])
+def test_scales_that_fp32_does_not_hold(scale, code):
+    """A scale that is infinite in fp32 would make NaN of every logit of 0."""
+    assert window(dict(WIN, Nq=0, scale=scale), q=None, out=None) == code
+    a = S.make_cache_attention_params(dict(ATTN, Nq=0, scale=scale))
+    assert S.lib.sparsepr_cache_attention(None, S.BF16, ctypes.byref(S.make_cache_params(CACHE)),
+                                          cache_pointers(), ctypes.byref(a), None, None, None, FAKE,
+                                          1 << 40, None) == code

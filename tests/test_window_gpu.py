@@ -347,3 +347,13 @@ def test_values_that_are_not_finite_under_vanishing_weights(H, Nk, weak, value):
     keep = [c for c in range(128) if c != 5]
     U.check(out[0][..., keep], lse[0], dict(ref, out=ref["out"][..., keep], mass=ref["mass"][..., keep]),
             q.dtype, 128, WEIGHTS)
+
+
+@pytest.mark.parametrize("scale", [1e-300, 1e-42, 1e-39])
+def test_scales_below_the_normal_numbers(scale):
+    """All visible keys weigh the same, and masked ones nothing."""
+    p = params(1, 2, 1, 200, 300, 64, window=70, sinks=2, scale=scale)
+    q, k, v = inputs(p, torch.bfloat16, 51)
+    out, lse, st = call(p, q, k, v)
+    assert st == 0
+    verify(p, q, k, v, out, lse)

@@ -83,7 +83,7 @@ struct DecodeMisc {
   float q[128];
 };
 static_assert(sizeof(DecodeMisc) <= 3072, "misc");
-static_assert(sizeof(LiteralScratch<kDecodeThreads>) <= 8192, "it shares the merge buffer");
+static_assert(sizeof(LiteralScratch<kDecodeThreads, 128>) <= 8192, "it shares the merge buffer");
 
 struct DecodeMaps {
   CUtensorMap k, v;  // [n_pages, Hkv * page, HD] bytes, boxes of min(page, tile) rows
@@ -167,14 +167,29 @@ struct PagedKV {
     const uint8_t* k = static_cast<const uint8_t*>(a.c.k8) +
                        (slot(j) * a.p.page + j % a.p.page) * D;
     float s_ = 0.f;
-    for (int c = 0; c < D; ++c) s_ = fmaf(q[c], from_e4m3(k[c]), s_);
+#pragma unroll 2
+    for (int c = 0; c < D; c += 16) {
+      float x[16];
+      from_e4m3_16(*reinterpret_cast<const uint4*>(k + c), x);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s_ = fmaf(q[c + e], x[e], s_);
+    }
     return s_ * a.c.k_scale[slot(j)];
   }
-  __device__ float v(int j, int c) const {
-    if (!page_at(j)) return __int_as_float(0x7fc00000);
-    const uint8_t* x = static_cast<const uint8_t*>(a.c.v8) +
-                       (slot(j) * a.p.page + j % a.p.page) * D;
-    return from_e4m3(x[c]) * a.c.v_scale[slot(j)];
+  __device__ void v(int j, int c, float (&x)[D / 32]) const {
+    if (!page_at(j)) {
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) x[e] = __int_as_float(0x7fc00000);
+      return;
+    }
+    const uint8_t* v8 = static_cast<const uint8_t*>(a.c.v8) +
+                        (slot(j) * a.p.page + j % a.p.page) * D + c;
+    const float scale = a.c.v_scale[slot(j)];
+    uint32_t w;
+    if (D == 128) w = *reinterpret_cast<const uint32_t*>(v8);
+    else w = *reinterpret_cast<const uint16_t*>(v8);
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) x[e] = from_e4m3((w >> (8 * e)) & 0xffu) * scale;
   }
 };
 
@@ -289,8 +304,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
   float* merge = reinterpret_cast<float*>(smem + L::merge_off);
   int* pre = reinterpret_cast<int*>(smem + L::pre_off);
   DecodeMisc& ms = *reinterpret_cast<DecodeMisc*>(smem + L::misc_off);
-  LiteralScratch<kDecodeThreads>& scratch =
-      *reinterpret_cast<LiteralScratch<kDecodeThreads>*>(smem + L::merge_off);
+  LiteralScratch<kDecodeThreads, HD>& scratch =
+      *reinterpret_cast<LiteralScratch<kDecodeThreads, HD>*>(smem + L::merge_off);
 
   // Put in place beside the tail of what came before on the stream, all of which is
   // waited for here; the combine kernel is put in place likewise as blocks end.

@@ -107,16 +107,17 @@ __device__ __forceinline__ void store_f32(float* p, float v) { *p = v; }
 // outside [0, s) and [lo, hi) touched. It is the reading of rows that meet
 // NaN or infinities (a product with a hidden NaN is NaN even at weight 0).
 //   kv.ok(j)      key j can be read
-//   kv.dot(j, q)  q . k_j            kv.v(j, c)  v_j[c]
+//   kv.dot(j, q)  q . k_j            kv.v(j, c, x)  x[e] = v_j[c + e], e < D / 32
 // Returns the maximum m (log2 units, sc = scale * log2 e), the sum l and, in
 // thread c < D, the unnormalised output o of column c; l is NaN for a row whose
 // visible logits are all -inf, and 0 for a row that sees nothing.
-// Called by the NT threads 0..NT-1 of a block, which `sync` joins.
-template <int NT>
+// Called by the NT threads 0..NT-1 of a block, which `sync` joins. A thread has a key of
+// its own in the first product, a warp in the second, every lane D / 32 columns of it.
+template <int NT, int D>
 struct LiteralScratch {
   float p[NT];
-  float o[NT];
-  float red[32];
+  float o[NT / 32][D];
+  float red[32], sum[32];
   int any[32];
 };
 
@@ -126,15 +127,14 @@ struct BlockSync {
 
 template <int NT, int D, class KV, class Sync>
 __device__ void literal_row(const KV& kv, const float* q, const Range r, float sc,
-                            LiteralScratch<NT>& sm, const Sync& sync, float& m_out, float& l_out,
+                            LiteralScratch<NT, D>& sm, const Sync& sync, float& m_out, float& l_out,
                             float& o_out) {
-  constexpr int kGroups = NT / D;
-  static_assert(kGroups >= 1 && NT % 32 == 0, "threads");
+  static_assert(NT % 32 == 0 && NT >= D, "threads");
+  constexpr int kWarpsHere = NT / 32, kC = D / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int total = r.s + (r.hi - r.lo);
-  float m = -INFINITY, l = 0.f, o = 0.f;
+  float m = -INFINITY, l = 0.f, o[kC] = {};
   bool seen = false;
-  const int c = tid % D, grp = tid / D;
   for (int base = 0; base < total; base += NT) {
     const int t = base + tid;
     bool on = false;
@@ -153,7 +153,7 @@ __device__ void literal_row(const KV& kv, const float* q, const Range r, float s
       sm.any[warp] = any;
     }
     sync();
-    for (int w = 0; w < NT / 32; ++w) {
+    for (int w = 0; w < kWarpsHere; ++w) {
       mx = fmaxf(mx, sm.red[w]);
       seen = seen || sm.any[w];
     }
@@ -163,34 +163,51 @@ __device__ void literal_row(const KV& kv, const float* q, const Range r, float s
     float p = -1.f;
     if (on) p = (mn == -INFINITY) ? (x == x ? 0.f : x) : exp2f(x - mn);
     sm.p[tid] = p;
+    float sum = p < 0.f ? 0.f : p;
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+    if (lane == 0) sm.sum[warp] = sum;
     sync();
-    float sum = 0.f;
-    const int n = min(NT, total - base);
-    for (int i = 0; i < n; ++i) {  // the same order in every thread
-      const float w = sm.p[i];
-      if (!(w < 0.f)) sum += w;
-    }
+    sum = 0.f;
+    for (int w = 0; w < kWarpsHere; ++w) sum += sm.sum[w];  // the same order in every thread
     l = l * corr + sum;
-    o *= corr;
-    if (grp < kGroups)
-      for (int i = grp; i < n; i += kGroups) {
-        const float w = sm.p[i];
-        if (w < 0.f) continue;
-        const int u = base + i;
-        o += w * kv.v(u < r.s ? u : r.lo + (u - r.s), c);
+#pragma unroll
+    for (int e = 0; e < kC; ++e) o[e] *= corr;
+    const int n = min(NT, total - base);
+    constexpr int kAhead = 8;  // keys in flight
+    for (int i0 = warp; i0 < n; i0 += kWarpsHere * kAhead) {
+      float w[kAhead], v[kAhead][kC];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int i = i0 + k * kWarpsHere, u = base + i;
+        w[k] = i < n ? sm.p[i] : -1.f;
+        if (w[k] < 0.f) {
+          w[k] = 0.f;
+#pragma unroll
+          for (int e = 0; e < kC; ++e) v[k][e] = 0.f;
+        } else {
+          kv.v(u < r.s ? u : r.lo + (u - r.s), lane * kC, v[k]);
+        }
       }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+        for (int e = 0; e < kC; ++e) o[e] += w[k] * v[k][e];
+    }
     m = mn;
     sync();
   }
-  sm.o[tid] = o;
+#pragma unroll
+  for (int e = 0; e < kC; ++e) sm.o[warp][lane * kC + e] = o[e];
   sync();
+  float all = 0.f;
   if (tid < D)
-    for (int g = 1; g < kGroups; ++g) o += sm.o[g * D + tid];
+    for (int w = 0; w < kWarpsHere; ++w) all += sm.o[w][tid];
   if (seen && l == 0.f) l = __int_as_float(0x7fc00000);
   sync();
   m_out = m;
   l_out = l;
-  o_out = o;
+  o_out = all;
 }
 
 }  // namespace spr

@@ -48,8 +48,8 @@ struct Smem {
   static constexpr int v_off = k_off + kStages * kTileBytes;
   static constexpr int bar_off = v_off + kStages * kTileBytes;
   static constexpr int ml_off = bar_off + 256;    // [2][2][128] row maxima and sums
-  static constexpr int flag_off = ml_off + 2048;  // [8] rows for the literal pass
-  static constexpr int bytes = flag_off + 32;
+  static constexpr int flag_off = ml_off + 2048;  // Flags
+  static constexpr int bytes = flag_off + 96;
 };
 // The d = 128 footprint for both head dims, so that one block runs per
 // multiprocessor (each takes all 512 columns of tensor memory); the tiles start
@@ -67,6 +67,16 @@ struct Bars {
   int abort;
 };
 static_assert(sizeof(Bars) <= 256, "barrier block");
+
+// Rows whose results need a second look.
+struct Flags {
+  uint32_t again[8];   // a bit a row: to be taken again by the definition
+  uint32_t values[8];  // a bit a row: a value of the result is not finite
+  // keys of the block's tiles with values that are not finite:
+  int last, first;     // the last one, the first one behind the sinks
+  uint32_t nan[4];     // columns that are NaN in a key that all rows of the unit see
+};
+static_assert(sizeof(Flags) <= 96, "flags");
 
 struct WindowMaps {
   CUtensorMap q, k, v;
@@ -160,6 +170,7 @@ struct TileKV {
   __device__ float dot(int j, const float* q) const {
     const uint4* row = reinterpret_cast<const uint4*>(k + static_cast<size_t>(j) * HD);
     float s = 0.f;
+#pragma unroll 4
     for (int c = 0; c < HD / 8; ++c) {
       const uint4 x = row[c];
       const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -171,8 +182,14 @@ struct TileKV {
     }
     return s;
   }
-  __device__ float v(int j, int c) const {
-    return load_f32(vals + static_cast<size_t>(j) * HD + c);
+  __device__ void v(int j, int c, float (&x)[HD / 32]) const {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(vals + static_cast<size_t>(j) * HD + c);
+#pragma unroll
+    for (int e = 0; e < HD / 64; ++e) {
+      const uint32_t y = w[e];
+      x[2 * e] = __uint_as_float(y << 16);
+      x[2 * e + 1] = __uint_as_float(y & 0xFFFF0000u);
+    }
   }
 };
 
@@ -226,10 +243,126 @@ __device__ __forceinline__ void unit_place(const WindowKernelParams& p, int unit
   if (p.a.see.causal) tile = p.tiles - 1 - tile;
 }
 
+// What the second look at rows needs of a block's unit.
+struct Unit {
+  UnitKeys keys;
+  int r0, i_last, len;
+  bool partial;
+  long long pos0;
+  int kvh;
+  size_t row_base, pbase;
+};
+
+// Rows whose result is not finite. It comes from values of the block's tiles that are not
+// finite. The result stands where the row sees all such keys, and where each of its columns
+// that are not finite is NaN in a key that all rows of the unit see. Else a key hidden from the
+// row may have done it (its weight is 0, but 0 times NaN is NaN), or a sum that left fp32, and
+// the row is taken again by the definition. (480p clip, 1.6 ms: with a NaN in the sink frame or
+// all values NaN 3.0 ms, with one in a middle frame, at whose ends units see it in part,
+// 70 ms; when every such row was taken again 1,635 and 544 ms.)
+template <int HD, typename T>
+__device__ __forceinline__ void look_again(const WindowKernelParams& p, const Unit& unit, uint8_t* smem,
+                                        Flags& flags) {
+  const WindowArgs& a = p.a;
+  const UnitKeys& u = unit.keys;
+  const size_t kvoff = static_cast<size_t>(unit.kvh) * a.Nk * HD;
+  const __nv_bfloat16* const kbase = static_cast<const __nv_bfloat16*>(a.k) + kvoff;
+  const __nv_bfloat16* const vbase = static_cast<const __nv_bfloat16*>(a.v) + kvoff;
+  auto range_of = [&](int i) { return visible_range(a.see, unit.pos0 + i, unit.len, p.by_frame); };
+  uint32_t doubtful = 0;
+  for (int w = 0; w < 8; ++w) doubtful |= flags.values[w];
+  if (doubtful) {
+    if (threadIdx.x == 0) {
+      flags.last = -1;
+      flags.first = 0x7fffffff;
+      for (int c = 0; c < 4; ++c) flags.nan[c] = 0;
+    }
+    __syncthreads();
+    // all rows of the unit see [0, common.s) and [common.lo, common.hi): its first query, or
+    // query 0 where rows go on from head to head, ends first, its last begins last
+    const Range begin = range_of(p.R != a.Nq ? 0 : unit.r0), end = range_of(unit.i_last);
+    const Range common = {begin.s, end.lo, begin.hi};
+    int last = -1, first = 0x7fffffff;
+    uint32_t nan = 0;  // of this thread's 8 columns
+    const int piece = threadIdx.x % (HD / 8);
+    static_assert(kThreads % (HD / 8) == 0, "a thread keeps to its columns");
+    for (int j = u.j0; j < u.j0 + u.T; ++j) {
+      const int k0 = u.start(j), k1 = u.end(j);
+      for (int key = k0 + static_cast<int>(threadIdx.x) / (HD / 8); key < k1; key += kThreads / (HD / 8)) {
+        const uint4 y = reinterpret_cast<const uint4*>(vbase + static_cast<size_t>(key) * HD)[piece];
+        const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+        uint32_t here = 0;
+        bool bad = false;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t x = (w[e >> 1] >> (16 * (e & 1))) & 0x7fffu;
+          bad = bad || x >= 0x7f80u;
+          here |= x > 0x7f80u ? 1u << e : 0u;
+        }
+        if (bad) {
+          last = max(last, key);
+          if (key >= end.s) first = min(first, key);
+          if (key < common.s || (key >= common.lo && key < common.hi)) nan |= here;
+        }
+      }
+    }
+    if (last >= 0) {
+      atomicMax(&flags.last, last);
+      atomicMin(&flags.first, first);
+      if (nan) atomicOr(&flags.nan[piece >> 2], nan << (8 * (piece & 3)));
+    }
+    __syncthreads();
+    const int ur = threadIdx.x;
+    if (ur < 256 && ((flags.values[ur >> 5] >> (ur & 31)) & 1u)) {
+      const Range rg = range_of(p.by_Nq.mod(unit.r0 + ur));
+      if (flags.last < 0 || flags.last >= rg.hi || (rg.s < rg.lo && flags.first < rg.lo)) {
+        bool explained = true;
+        for (int c = 0; c < HD; ++c) {
+          const float x = unit.partial ? p.opart[(unit.pbase + ur) * HD + c]
+                                       : load_f32(static_cast<const T*>(a.out) + (unit.row_base + ur) * HD + c);
+          if (!(fabsf(x) < INFINITY)) explained = explained && ((flags.nan[c >> 5] >> (c & 31)) & 1u);
+        }
+        if (!explained) atomicOr(&flags.again[ur >> 5], 1u << (ur & 31));
+      }
+    }
+    __syncthreads();
+  }
+  LiteralScratch<kThreads, HD>& scratch = *reinterpret_cast<LiteralScratch<kThreads, HD>*>(smem);
+  static_assert(sizeof(scratch) <= 8192, "the query lies behind it");
+  float* q = reinterpret_cast<float*>(smem + 8192);
+  for (int w = 0; w < 8; ++w) {
+    uint32_t todo = flags.again[w];
+    while (todo) {
+      const int ur = w * 32 + __ffs(todo) - 1;
+      todo &= todo - 1;
+      const size_t row = unit.row_base + ur;
+      const TileKV<HD> kv = {kbase, vbase, u};
+      for (int c = threadIdx.x; c < HD; c += kThreads)
+        q[c] = load_f32(static_cast<const __nv_bfloat16*>(a.q) + row * HD + c);
+      __syncthreads();
+      float m, l, o;
+      literal_row<kThreads, HD>(kv, q, range_of(p.by_Nq.mod(unit.r0 + ur)), a.sc, scratch, BlockSync{},
+                                m, l, o);
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const float lsev = l == 0.f ? -INFINITY : m + log2f(l);
+      if (threadIdx.x < HD) {
+        if (unit.partial) p.opart[(unit.pbase + ur) * HD + threadIdx.x] = o * inv;
+        else store_f32(static_cast<T*>(a.out) + row * HD + threadIdx.x, o * inv);
+      }
+      if (threadIdx.x == 0) {
+        if (unit.partial) p.lpart[unit.pbase + ur] = lsev;
+        else if (a.lse) a.lse[row] = lsev * kLn2F;
+      }
+      __syncthreads();
+    }
+  }
+}
+
 // T: the output type; the inputs are bf16.
 template <int HD, typename T>
 __global__ void __launch_bounds__(kThreads, 1)
-    window_attn_kernel(const __grid_constant__ WindowMaps maps, const WindowKernelParams p) {
+    window_attn_kernel(const __grid_constant__ WindowMaps maps,
+                       const __grid_constant__ WindowKernelParams p) {
   using L = Smem<HD>;
   constexpr int kAtoms = HD / 64;
   const WindowArgs& a = p.a;
@@ -309,12 +442,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   // tasks of warpgroup i: two query tiles -> every key tile; one -> tiles 2t + i
   const bool two = nq == 2;
   const int ntask[2] = {two ? T_tiles : (T_tiles + 1) / 2, two ? T_tiles : T_tiles / 2};
-  // A tile that ends behind the sequence holds rows of V that may be anything,
-  // also NaN, and a weight of 0 does not silence them: the V warp clears them.
-  // (Rows behind the buffer are zero already: TMA fills them.) At most the last
-  // tile of each key range is such a tile.
+  // A tile that ends behind its key range holds rows of V that no row of the unit sees. They
+  // may be anything, also NaN, and a weight of 0 does not silence them: the V warp clears them.
+  // (Rows behind the buffer are zero already: TMA fills them.) At most the last tile of each
+  // key range is such a tile.
   auto needs_fix = [&](int j) {
-    return u.start(j) + kTileN > len && (len < a.Nk || p.kv_box_rows < kTileN);
+    const int end = u.end(j);
+    return u.start(j) + kTileN > end && (end < a.Nk || p.kv_box_rows < kTileN);
   };
 
   extern __shared__ uint8_t smem_raw[];
@@ -325,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* Vs = smem + L::v_off;
   Bars* bars = reinterpret_cast<Bars*>(smem + L::bar_off);
   float* ml = reinterpret_cast<float*>(smem + L::ml_off);
-  uint32_t* flags = reinterpret_cast<uint32_t*>(smem + L::flag_off);
+  Flags& flags = *reinterpret_cast<Flags*>(smem + L::flag_off);
 
   if (threadIdx.x == 9 * 32) {  // while warp 0 takes tensor memory
     mbar_init(&bars->q_full[0], 1);
@@ -348,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bars->abort = 0;
     fence_barrier_init();
   }
-  if (threadIdx.x < 8) flags[threadIdx.x] = 0;
+  if (threadIdx.x < 16) flags.again[threadIdx.x] = 0;  // and flags.values
   if (warp == 0) {
     tmem_alloc(&bars->tmem_base, kTmemCols);
     tmem_relinquish();
@@ -393,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = mbar_wait(&full[st], (j / kStages) & 1, abort);
         if (!__all_sync(0xffffffffu, ok)) break;
         for (int c = 0; c < kAtoms; ++c)
-          for (int x = (len - k0) * 8 + lane; x < kTileN * 8; x += 32)
+          for (int x = (u.end(j0 + j) - k0) * 8 + lane; x < kTileN * 8; x += 32)
             *reinterpret_cast<uint4*>(ring + st * L::kTileBytes + c * L::kSlab + x * 16) =
                 make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
@@ -601,7 +735,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the whole number k of log2 units that brings its largest value to at
       // most 1: its values are formed again, and the row sum and O are scaled
       // by 2^-k, exactly. O and the row sum always share one reference, so the
-      // result is exact.
+      // result is exact. The sum stays finite, and NaN in it comes from a visible logit that
+      // is NaN or +inf: the row's softmax is NaN then.
       if (__any_sync(0xffffffffu, m_ref == -INFINITY)) {
         load_half(0);
         const float m0 = half_max();
@@ -613,12 +748,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int hf = 0; hf < 2; ++hf) {
         load_half(hf);
         float rh = exp_half(m_ref);
-        const bool over = live && rh > kOverflowSum;  // NaN goes to the literal pass
+        const bool over = live && rh > kOverflowSum;
         if (__any_sync(0xffffffffu, over)) {
           load_half(hf);
           float sh = 1.f;  // 2^-k, formed from its bits (0 when k >= 127)
           if (over) {
-            const float k = fminf(ceilf(half_max() - m_ref), 16384.f);
+            const float k = ceilf(half_max() - m_ref);
             sh = (k < 127.f) ? __int_as_float((127 - static_cast<int>(k)) << 23) : 0.f;
             m_ref += k;
           }
@@ -654,11 +789,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------- epilogue: O / l -> global -------------------------------
     float f0, f1 = 0.f, lsev;  // factors of this thread's O and the other one's, log2-sum-exp
     bool has1 = false, use0 = false, use1 = false;  // one tile: halves that hold keys of the row
+    bool lost;  // the row's softmax is NaN
     if (two) {
-      f0 = live && l_sum > 0.f ? 1.f / l_sum : 0.f;
+      lost = live && l_sum != l_sum;
+      f0 = lost ? l_sum : live && l_sum > 0.f ? 1.f / l_sum : 0.f;
       lsev = live && l_sum > 0.f ? m_ref + __log2f(l_sum) : -INFINITY;
-      if (live && seen && (l_sum == 0.f || !(l_sum < INFINITY) || !(fabsf(m_ref) < kMaxReference)))
-        atomicOr(&flags[ur >> 5], 1u << (ur & 31));
+      if (live && !lost && seen && (l_sum == 0.f || !(l_sum < INFINITY) || !(fabsf(m_ref) < kMaxReference)))
+        atomicOr(&flags.again[ur >> 5], 1u << (ur & 31));
       ok = ok && mbar_wait(&bars->o_done[i], 0, abort);
     } else {
       // merge the two halves of the key tiles: each warpgroup writes half of
@@ -669,6 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float m0 = ml[row], l0 = ml[kTileM + row];
       const float m1 = ml[2 * kTileM + row], l1 = ml[3 * kTileM + row];
       has1 = ntask[1] > 0;
+      lost = live && (l0 != l0 || (has1 && l1 != l1));
       const float mm = has1 ? fmaxf(m0, m1) : m0;
       // a half that holds none of the row's keys has the reference -inf
       use0 = m0 != -INFINITY;
@@ -677,15 +815,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float a1 = use1 ? ex2_approx(m1 - mm) : 0.f;
       const float l = l0 * a0 + (has1 ? l1 * a1 : 0.f);
       const bool far = mm != -INFINITY && !(fabsf(mm) < kMaxReference);
-      const float inv = live && l > 0.f ? 1.f / l : 0.f;
+      const float inv = lost ? __int_as_float(0x7fc00000) : live && l > 0.f ? 1.f / l : 0.f;
+      use0 = use0 || lost;
       f0 = a0 * inv;
       f1 = a1 * inv;
       lsev = live && l > 0.f ? mm + __log2f(l) : -INFINITY;
-      if (live && ((seen && l == 0.f) || !(l < INFINITY) || far))
-        atomicOr(&flags[ur >> 5], 1u << (ur & 31));
+      if (live && !lost && ((seen && l == 0.f) || !(l < INFINITY) || far))
+        atomicOr(&flags.again[ur >> 5], 1u << (ur & 31));
       ok = ok && mbar_wait(&bars->o_done[0], 0, abort);
       if (has1) ok = ok && mbar_wait(&bars->o_done[1], 0, abort);
     }
+    if (lost) lsev = __int_as_float(0x7fc00000);
     if (__all_sync(0xffffffffu, ok)) {
       tc_fence_after();
       const bool leads = two || i == 0;
@@ -736,7 +876,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           else RowStage<T, HD>::flush(stage, lane, out + (row_base + ur0) * HD + col, rows);
         }
       }
-      if (live && !finite) atomicOr(&flags[ur >> 5], 1u << (ur & 31));
+      if (live && !lost && !finite) atomicOr(&flags.values[ur >> 5], 1u << (ur & 31));
     }
   }
   __syncthreads();
@@ -748,39 +888,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_dealloc(tmem, kTmemCols);
   }
   if (aborted) return;
-  // Rows whose result is not finite: a hidden key with NaN or infinity in the same
-  // tile, or a visible one. They are taken again by the definition.
-  LiteralScratch<kThreads>& scratch = *reinterpret_cast<LiteralScratch<kThreads>*>(smem);
-  float* q = reinterpret_cast<float*>(smem + 8192);
-  for (int w = 0; w < 8; ++w) {
-    uint32_t todo = flags[w];
-    while (todo) {
-      const int ur = w * 32 + __ffs(todo) - 1;
-      todo &= todo - 1;
-      const size_t row = row_base + ur;
-      const __nv_bfloat16* kbase = static_cast<const __nv_bfloat16*>(a.k);
-      const __nv_bfloat16* vbase = static_cast<const __nv_bfloat16*>(a.v);
-      const size_t kvoff = static_cast<size_t>(kvh) * a.Nk * HD;
-      const TileKV<HD> kv = {kbase + kvoff, vbase + kvoff, u};
-      for (int c = threadIdx.x; c < HD; c += kThreads)
-        q[c] = load_f32(static_cast<const __nv_bfloat16*>(a.q) + row * HD + c);
-      __syncthreads();
-      float m, l, o;
-      literal_row<kThreads, HD>(kv, q, visible_range(a.see, pos0 + p.by_Nq.mod(r0 + ur), len, p.by_frame), a.sc,
-                                scratch, BlockSync{}, m, l, o);
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      const float lsev = l == 0.f ? -INFINITY : m + log2f(l);
-      if (threadIdx.x < HD) {
-        if (partial) p.opart[(pbase + ur) * HD + threadIdx.x] = o * inv;
-        else store_f32(out + row * HD + threadIdx.x, o * inv);
-      }
-      if (threadIdx.x == 0) {
-        if (partial) p.lpart[pbase + ur] = lsev;
-        else if (a.lse) a.lse[row] = lsev * kLn2F;
-      }
-      __syncthreads();
-    }
-  }
+  uint32_t any = 0;
+  for (int w = 0; w < 8; ++w) any |= flags.again[w] | flags.values[w];
+  if (any)
+    look_again<HD, T>(p, Unit{u, r0, i_last, len, partial, pos0, kvh, row_base, pbase}, smem, flags);
 }
 
 // out = sum_s 2^(l_s - M) O_s / sum_s 2^(l_s - M), M = max_s l_s, over the splits'

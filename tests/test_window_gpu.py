@@ -357,3 +357,86 @@ def test_scales_below_the_normal_numbers(scale):
     out, lse, st = call(p, q, k, v)
     assert st == 0
     verify(p, q, k, v, out, lse)
+
+
+@pytest.mark.parametrize("bad", ["values", "keys", "both"])
+@pytest.mark.parametrize("p", [
+    params(1, 2, 1, 700, 700, 128, window=150, sinks=3), params(1, 3, 1, 40, 900, 64, window=300, sinks=5),
+    params(1, 1, 1, 600, 600, 64, frame=50, window=3, sinks=1, causal=0),
+    params(1, 2, 2, 300, 300, 128, frame=130, window=1, sinks=2),
+    params(2, 4, 2, 257, 511, 128, causal=0), params(1, 1, 1, 500, 500, 128),
+    params(1, 2, 2, 3, 4000, 64, window=3900), params(1, 1, 1, 300, 200, 64, window=60, sinks=1)])
+def test_nan_shows_where_it_is_seen_and_nowhere_else(p, bad):
+    """NaN values in single columns, and NaN keys, seen by some rows and hidden from others
+    of the same tile."""
+    q, k, v = inputs(p, torch.bfloat16, 61)
+    rng = np.random.default_rng(p["Nk"])
+    for b in range(p["B"]):
+        for h in range(p["Hkv"]):
+            for j in rng.integers(0, p["Nk"], 4):
+                if bad != "keys":
+                    v[b, h, int(j), int(rng.integers(p["d"]))] = float("nan")
+            if bad != "values":
+                k[b, h, int(rng.integers(p["Nk"])), 3] = float("nan")
+    out, lse, st = call(p, q, k, v)
+    assert st == 0
+    verify(p, q, k, v, out, lse)
+
+
+@pytest.mark.parametrize("causal", [0, 1])
+@pytest.mark.parametrize("d", [64, 128])
+def test_what_every_row_sees_costs_no_second_pass(d, causal):
+    """A NaN and an infinity in the sink frame, and a NaN key there: columns that they do not
+    touch are those of the call without them, bit for bit, and the calls take no more than
+    a few times as long (rows taken again one by one took 100 to 250 times as long here). So
+    are rows from whose tiles a NaN is hidden altogether, though it lies right behind the sinks."""
+    p = params(1, 2, 1, 4000, 4000, d, frame=200, window=3, sinks=1, causal=causal)
+    q, k, v = inputs(p, torch.bfloat16, 5)
+    ws = S.allocate_window_workspace(p, q.dtype)
+    out, lse = torch.zeros_like(q), torch.zeros(q.shape[:3], device="cuda")
+
+    def go(k, v):
+        for _ in range(2):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            torch.cuda.synchronize()
+            a.record()
+            S.sparsepr_window_attention(q, k, v, p, out, ws, lse=lse)
+            b.record()
+            torch.cuda.synchronize()
+        return out.clone(), lse.clone(), a.elapsed_time(b)
+    clean, clean_lse, t0 = go(k, v)
+    v2, k2 = v.clone(), k.clone()
+    v2[0, 0, 7, 5], v2[0, 0, 9, 6], k2[0, 0, 7, 5] = float("nan"), float("inf"), float("nan")
+    got, got_lse, t1 = go(k, v2)
+    keep = [c for c in range(d) if c not in (5, 6)]
+    assert torch.isnan(got[..., 5]).all() and (got[..., 6] == float("inf")).all()
+    assert torch.equal(got_lse, clean_lse) and torch.equal(got[..., keep], clean[..., keep])
+    got, got_lse, t2 = go(k2, v)
+    assert torch.isnan(got).all() and torch.isnan(got_lse).all()
+    v3 = v.clone()
+    v3[0, 0, 210] = float("nan")  # frame 1: seen up to frame 3
+    got, got_lse, _ = go(k, v3)
+    assert torch.isnan(got[:, :, 200:800]).all() and torch.isfinite(got[:, :, 800:]).all()
+    # (rows 800 to 1023 share their unit with rows that see it, and are taken again)
+    assert torch.equal(got[:, :, 1024:], clean[:, :, 1024:])
+    assert torch.equal(got_lse[:, :, 1024:], clean_lse[:, :, 1024:])
+    got, _, t3 = go(k, torch.full_like(v, float("nan")))
+    assert torch.isnan(got).all()
+    assert max(t1, t2, t3) < 20 * t0, (t0, t1, t2, t3)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_leaps_of_logits(d):
+    """Logits that leap by 20,000 and more log2 units between groups of keys: whole numbers up
+    to 2^14 and a little, which fp32 sums exactly. (Not further: at 2^24 fp32 rounds the logits
+    themselves by whole units, and the bounds, linear in that rounding, say nothing.)"""
+    p = params(1, 2, 1, 600, 600, d, scale=1.0)
+    q, k, v = inputs(p, torch.bfloat16, 71)
+    q, k = torch.round(q), torch.round(k)
+    q[..., 0] = 16.0
+    for n, x in ((0, -1024.0), (200, 0.0), (300, 1024.0)):
+        k[:, :, n:, 0] = x
+    q[:, 1, :, 0] = -16.0  # the other head leaps down
+    out, lse, st = call(p, q, k, v)
+    assert st == 0
+    verify(p, q, k, v, out, lse)

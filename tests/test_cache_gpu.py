@@ -663,3 +663,69 @@ def test_append_of_nothing_beside_a_shared_page():
     S.sparsepr_cache_append(x, x, p, r.c, U.i32([20, 7, 64, 40]), U.i32([0, 0, 0, 0]), r.ws)
     assert r.status() == 0
     r.same()
+
+
+@pytest.mark.parametrize("Nq,kw", [(1, {}), (5, {}), (3, dict(window=120, sinks=20)),
+                                   (16, dict(frame=7, window=9, sinks=1)), (40, dict(window=70, sinks=3))])
+@pytest.mark.parametrize("d", [64, 128])
+def test_nan_shows_where_it_is_seen_and_nowhere_else(d, Nq, kw):
+    """NaN values in single columns and NaN keys, early, in the window and among the last
+    tokens, of which some queries see some."""
+    p = cache_params(3, 2, d, 16, 80, 24)
+    r = Run(p, 31)
+    r.grow([300, 200, 90])
+    rng = np.random.default_rng(d + Nq)
+    for b, L in enumerate((300, 200, 90)):
+        for j in [3, int(rng.integers(L)), L - 1 - int(rng.integers(4)), L - 1]:
+            r.c.v8.view(torch.uint8)[int(r.m.table[b, j // 16]), b % 2, j % 16, int(rng.integers(d))] = 0x7F
+        j = int(rng.integers(L))
+        if b:
+            r.c.k8.view(torch.uint8)[int(r.m.table[b, j // 16]), 0, j % 16, 3] = 0xFF
+    r.m = U.to_model(p, r.c)
+    assert r.attend(dict(Hq=4, Nq=Nq, **kw)) == 0
+
+
+@pytest.mark.parametrize("Nq", [1, 8])
+@pytest.mark.parametrize("d", [64, 128])
+def test_what_every_query_sees_costs_no_second_pass(d, Nq):
+    """A NaN in the first token: columns that it does not touch are those of the call without
+    it, bit for bit; so are the other heads' where a key is NaN. Neither takes more than a few
+    times as long (taken again one by one, rows took 100 times as long and more)."""
+    p = cache_params(8, 4, d, 64, 8 * 64, 64)
+    r = Run(p)
+    c = r.c
+    g = torch.Generator(device="cuda").manual_seed(1)
+    for t in (c.k8, c.v8):
+        t.copy_((torch.randn(t.shape, generator=g, device="cuda") * 90).clamp_(-448, 448).to(S.F8))
+    c.k_scale.fill_(2.0 ** -6), c.v_scale.fill_(2.0 ** -6)
+    c.table.copy_(torch.arange(512, dtype=torch.int32, device="cuda").view(8, 64))
+    c.len.fill_(4000), c.ref.fill_(1)
+    attn = dict(Hq=4, Nq=Nq)
+    q = U.normal((8, 4, Nq, d), 3)
+    out, lse = torch.zeros_like(q), torch.zeros(q.shape[:3], device="cuda")
+    ws = S.allocate_cache_workspace(p, attn)
+
+    def go():
+        for _ in range(2):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            torch.cuda.synchronize()
+            a.record()
+            S.sparsepr_cache_attention(q, p, c, attn, out, ws, lse=lse)
+            b.record()
+            torch.cuda.synchronize()
+        return out.clone(), lse.clone(), a.elapsed_time(b)
+    clean, clean_lse, t0 = go()
+    assert torch.isfinite(clean).all()
+    c.v8.view(torch.uint8)[::64, :, 7, 5] = 0x7F
+    got, got_lse, t1 = go()
+    keep = [i for i in range(d) if i != 5]
+    assert torch.isnan(got[..., 5]).all() and torch.equal(got_lse, clean_lse)
+    assert torch.equal(got[..., keep], clean[..., keep])
+    c.k8.view(torch.uint8)[::64, 2, 9, 3] = 0x7F
+    got, got_lse, t2 = go()
+    assert torch.isnan(got[:, 2]).all() and torch.isnan(got_lse[:, 2]).all()
+    assert torch.equal(got[:, :2][..., keep], clean[:, :2][..., keep])
+    c.table[:, 3] = -1  # pages that are missing
+    got, _, t3 = go()
+    assert torch.isnan(got).all() and U.status(ws) == 1 << S.ERR_INVALID_ARG
+    assert max(t1, t2, t3) < 20 * t0, (t0, t1, t2, t3)

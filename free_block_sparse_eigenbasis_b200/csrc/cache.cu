@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(128) evict_kernel(const CacheArgs a, sparsepr_
   give_up(a, b, static_cast<int>(j0), static_cast<int>(j1));
 }
 
-// Plan of the packing: counts[0] moves, pages[i] -> targets[i]. One block: the plan is a
+// Plan of the packing: counts[0] moves, pages[i] -> targets[i], remap[pages[i]] = i. One block: the plan is a
 // scan over the pool's counts, 4,096 pages a round.
 __global__ void __launch_bounds__(kPlanThreads)
     compact_plan_kernel(const CacheArgs a, int32_t* n_used) {
@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kPlanThreads)
       for (int e = 0; e < kPerThread; ++e) r[e] = next[e];
   }
   __syncthreads();
-  for (int i = tid; i < moves; i += kPlanThreads) a.remap[a.pages[i]] = a.targets[i];
+  for (int i = tid; i < moves; i += kPlanThreads) a.remap[a.pages[i]] = i;
   if (tid == 0) {
     a.counts[0] = moves;
     a.counts[1] = used;
@@ -317,10 +317,10 @@ __global__ void __launch_bounds__(kCopyThreads) compact_move_kernel(const CacheA
   for (long long i = static_cast<long long>(blockIdx.x) * kCopyThreads + threadIdx.x; i < entries;
        i += static_cast<long long>(gridDim.x) * kCopyThreads) {
     const int id = a.c.table[i];
-    // an entry without a page count is not one of the moved pages
-    if (id >= used && id < a.p.n_pages && moves > 0) {
-      const int to = a.remap[id];
-      a.c.table[i] = to;
+    // (an entry whose page has no count is none of the moves, and remap holds nothing for it)
+    if (id >= used && id < a.p.n_pages) {
+      const int move = a.remap[id];
+      if (move >= 0 && move < moves && a.pages[move] == id) a.c.table[i] = a.targets[move];
     }
   }
   const int pieces = a.p.Hkv * (a.p.page * a.p.d / 16);

@@ -355,7 +355,7 @@ struct CacheArgs {
   int32_t* counts;   // [16]
   int32_t* pages;    // [n_pages] free pages (reserve), pages that move (compact)
   int32_t* targets;  // [n_pages] where they go (compact)
-  int32_t* remap;    // [n_pages] (compact)
+  int32_t* remap;    // [n_pages] which move a page is (compact)
   int32_t* copies;   // [2, B] source and target of the copied last pages (reserve)
   int sm_count;
 };

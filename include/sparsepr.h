@@ -572,7 +572,7 @@ sparsepr_status sparsepr_cache_evict(const sparsepr_cache_params* p, const spars
 /* Pack the pool: with n pages in use, the i-th page in use at n or above moves
  * to the i-th free page below n (both ascending); table and ref follow, so that
  * the pages in use are 0..n-1. n_used: [1] int32 device, receives n. Bytes of the
- * pages left behind stay. */
+ * pages left behind stay, and so do entries that name a page with ref 0. */
 sparsepr_status sparsepr_cache_compact(const sparsepr_cache_params* p, const sparsepr_cache* c,
                                        int32_t* n_used, void* ws, size_t ws_bytes, void* stream);
 

@@ -729,3 +729,21 @@ def test_what_every_query_sees_costs_no_second_pass(d, Nq):
     got, _, t3 = go()
     assert torch.isnan(got).all() and U.status(ws) == 1 << S.ERR_INVALID_ARG
     assert max(t1, t2, t3) < 20 * t0, (t0, t1, t2, t3)
+
+
+@pytest.mark.parametrize("stale", [0x00, 0x01, 0x55, 0xFF])
+def test_packing_leaves_entries_without_a_count(stale):
+    """An entry that names a page with ref 0, whatever the workspace held."""
+    p = cache_params(3, 1, 64, 16, 300, 4)
+    r = Run(p)
+    r.grow([40, 30, 20])
+    S.sparsepr_cache_free(U.i32([0]), p, r.c, r.ws)
+    r.m.free([0])
+    for t in (r.c.table, r.m.table):
+        t[0, 3], t[0, 1], t[2, 3] = 7, 299, 6  # page 6 moves, and so does this entry of it
+    r.ws[256:].fill_(stale)
+    used = U.i32([0])
+    S.sparsepr_cache_compact(p, r.c, used, r.ws)
+    assert int(used) == r.m.compact()
+    assert r.c.table[0].tolist() == [-1, 299, -1, 7]
+    r.same()

@@ -1,5 +1,9 @@
 """The paged 8-bit cache on the GPU: pages, scales and codes against the host
 model bit for bit, attention against the fp64 oracle, and a whole rollout."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -747,3 +751,46 @@ def test_packing_leaves_entries_without_a_count(stale):
     assert int(used) == r.m.compact()
     assert r.c.table[0].tolist() == [-1, 299, -1, 7]
     r.same()
+
+
+def test_first_calls_of_a_process_inside_captures():
+    """A process whose first call of every attention kernel is captured: whatever a kernel
+    needs once per device is set up in the capture."""
+    code = """
+import torch
+from free_block_sparse_eigenbasis_b200 import sparsepr as S
+for d in (64, 128):
+    p = dict(B=2, Hkv=1, d=d, page=32, n_pages=8, max_pages=4)
+    c = S.allocate_cache(p)
+    for t in (c.k8, c.v8):
+        t.copy_(torch.randn(t.shape, device="cuda").to(S.F8))
+    c.table.copy_(torch.arange(8, dtype=torch.int32, device="cuda").view(2, 4))
+    c.len.fill_(100), c.ref.fill_(1)
+    for dtype in (torch.bfloat16, torch.float32):
+        for rows in (3, 12, 90):  # in place, 8 and 16 rows a unit, and widened
+            q = torch.randn(2, 3, rows // 3, d, device="cuda").to(dtype)
+            a = dict(Hq=3, Nq=rows // 3)
+            calls = [(S.allocate_cache_workspace(p, a), lambda out, ws, q=q, a=a:
+                      S.sparsepr_cache_attention(q, p, c, a, out, ws))]
+            if rows == 90:  # the windowed kernel's own first call, before the cache's
+                k = torch.randn(2, 1, 700, d, device="cuda").to(dtype)
+                w = dict(B=2, Hq=3, Hkv=1, Nq=30, Nk=700, d=d)
+                calls.insert(0, (S.allocate_window_workspace(w, dtype), lambda out, ws, q=q, k=k, w=w:
+                                 S.sparsepr_window_attention(q, k, k, w, out, ws)))
+            for ws, call in calls:
+                out, again = torch.zeros_like(q), torch.zeros_like(q)
+                torch.cuda.synchronize()
+                g = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(g):
+                    call(out, ws)
+                g.replay()
+                torch.cuda.synchronize()
+                call(again, ws)
+                assert torch.equal(out, again) and out.abs().sum() > 0
+                assert int(ws[:4].view(torch.int32)) == 0
+print("captured")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]

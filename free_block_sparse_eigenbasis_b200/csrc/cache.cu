@@ -369,8 +369,9 @@ constexpr int kAppendThreads = 128;
 // page and head share a scale. The new tokens of a page and head are contiguous in
 // the input and in the page: first their largest magnitude, then, with the values
 // still in the first-level cache (32 KB at most), their rounding. Bound by latency at
-// the sizes of a step: one token of 8 sequences 2.6 us, a frame of 1,560 tokens and
-// 12 heads (14.4 MB) 5.0 us, one call behind the other in a graph.
+// the sizes of a step: one token of 8 sequences 2.5 us, a frame of 1,560 tokens and
+// 12 heads (14.4 MB) 5.0 us (a sixteenth of a replayed graph of 16 such calls; called one by
+// one from Python either takes 12 us, which is the host's time).
 template <typename T>
 __global__ void __launch_bounds__(kAppendThreads)
     append_kernel(const CacheArgs a, const void* k, const void* v, int T_rows,

@@ -298,9 +298,9 @@ __device__ __forceinline__ int blocks_for(long long total) {
 // product's operand by an 8x8 transpose.
 //
 // Bound by the stream of pages where there is much to read (32 sequences of up to
-// 8,192 tokens, 8 key heads: 85.6 us, 4.3 TB/s; 72 us without the arithmetic), else by
+// 8,192 tokens, 8 key heads: 86.8 us, 4.2 TB/s; 72 us without the arithmetic), else by
 // latency: a block's run takes about 7 us around its first tiles (12 heads of 1,000 tokens:
-// 18.5 us with the combine). Two blocks of six warps hide one another's ends: one block of
+// 17.7 us with the combine). Two blocks of six warps hide one another's ends: one block of
 // twelve took 105 us.
 template <int HD, int NT, typename T>
 __global__ void __launch_bounds__(kDecodeThreads, 2)

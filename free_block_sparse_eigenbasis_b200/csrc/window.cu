@@ -17,7 +17,7 @@
 // in tensor memory.
 //
 // Bound by the tensor cores with their shared-memory operands: 480p clip (12 heads,
-// 32,760 rows, 9,360 keys each at most) 1.51 to 1.70 ms, 1,030 to 1,160 TFLOP/s of
+// 32,760 rows, 9,360 keys each at most) 1.45 to 1.70 ms, 1,030 to 1,210 TFLOP/s of
 // visible pairs, 60% of the tensor cycles at the 1.7 GHz that the power limit leaves;
 // 1.35 ms with no softmax at all, 1.50 ms without the copies of K and V (of 1.55). Tiles of
 // 128 x 128, because a product with 64 columns takes as long as one with 128.

@@ -451,7 +451,8 @@ size_t sparsepr_window_workspace_bytes(const sparsepr_window_params* p, sparsepr
  *   lse  [B, Hq, Nq] fp32 or NULL: natural log of the sum of exponentials
  * Rows of out and lse behind a sequence's n_q rows are not written; rows of
  * k and v behind n_k are not used. MMAs in bf16 with fp32 accumulation for
- * both dtypes (fp32 inputs are rounded to bf16 first), softmax in fp32.
+ * both dtypes (fp32 inputs are rounded to bf16 in ws first, all rows of the
+ * buffers on every call), softmax in fp32.
  * Values of n_q outside [0, Nq] or of n_k outside [0, Nk] raise
  * SPARSEPR_ERR_INVALID_ARG in the status word and are clamped. */
 sparsepr_status sparsepr_window_attention(const void* q, const void* k, const void* v,
@@ -494,7 +495,10 @@ typedef struct {
 
 /* Bytes of workspace of the cache calls; with `a` NULL of all but
  * sparsepr_cache_attention (0: invalid parameters). A workspace that serves
- * an attention serves the other calls too. */
+ * an attention serves the other calls too. Beyond 32 query rows per key head an
+ * attention takes room for the tokens of whole table rows in bf16 (4 Hkv d max_pages page
+ * bytes a sequence, whatever the visibility), for as many sequences at a time as fit 1 GB,
+ * but one at least; more sequences are worked on in turn. */
 size_t sparsepr_cache_workspace_bytes(const sparsepr_cache_params* p,
                                       const sparsepr_cache_attention_params* a);
 
@@ -519,7 +523,8 @@ sparsepr_status sparsepr_cache_reserve(const sparsepr_cache_params* p, const spa
  * sequence (start inside the page) it is the larger of that and the page's
  * scale, and if it grows, the earlier tokens are rounded again to the new scale
  * (exact but for values that fall below 2^-6 s). Values are rounded to
- * nearest even; NaN and infinities are stored as NaN and do not enter the
+ * nearest even (at s = 2^120 magnitudes from 248 s, 3.3e38, on round to 256 s = 2^128
+ * and are infinite when read); NaN and infinities are stored as NaN and do not enter the
  * scale. Does not read or change len. start[b] < 0 skips the sequence. An entry
  * without a page, a page with ref != 1, n_new outside [0, T] or tokens past the
  * table raise SPARSEPR_ERR_INVALID_ARG and are not written. */

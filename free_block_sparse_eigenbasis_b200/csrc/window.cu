@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bars->abort = 0;
     fence_barrier_init();
   }
-  if (threadIdx.x < 16) flags.again[threadIdx.x] = 0;  // and flags.values
+  if (threadIdx.x < 8) flags.again[threadIdx.x] = flags.values[threadIdx.x] = 0;
   if (warp == 0) {
     tmem_alloc(&bars->tmem_base, kTmemCols);
     tmem_relinquish();

@@ -710,14 +710,16 @@ def test_what_every_query_sees_costs_no_second_pass(d, Nq):
     ws = S.allocate_cache_workspace(p, attn)
 
     def go():
-        for _ in range(2):
+        best = 1e9
+        for _ in range(6):
             a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
             torch.cuda.synchronize()
             a.record()
             S.sparsepr_cache_attention(q, p, c, attn, out, ws, lse=lse)
             b.record()
             torch.cuda.synchronize()
-        return out.clone(), lse.clone(), a.elapsed_time(b)
+            best = min(best, a.elapsed_time(b))
+        return out.clone(), lse.clone(), best
     clean, clean_lse, t0 = go()
     assert torch.isfinite(clean).all()
     c.v8.view(torch.uint8)[::64, :, 7, 5] = 0x7F

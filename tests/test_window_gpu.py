@@ -396,14 +396,16 @@ def test_what_every_row_sees_costs_no_second_pass(d, causal):
     out, lse = torch.zeros_like(q), torch.zeros(q.shape[:3], device="cuda")
 
     def go(k, v):
-        for _ in range(2):
+        best = 1e9
+        for _ in range(6):
             a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
             torch.cuda.synchronize()
             a.record()
             S.sparsepr_window_attention(q, k, v, p, out, ws, lse=lse)
             b.record()
             torch.cuda.synchronize()
-        return out.clone(), lse.clone(), a.elapsed_time(b)
+            best = min(best, a.elapsed_time(b))
+        return out.clone(), lse.clone(), best
     clean, clean_lse, t0 = go(k, v)
     v2, k2 = v.clone(), k.clone()
     v2[0, 0, 7, 5], v2[0, 0, 9, 6], k2[0, 0, 7, 5] = float("nan"), float("inf"), float("nan")

@@ -64,7 +64,7 @@ struct DecodeSmem {
                                          ? merge_bytes / (kRegs * 128) : kWarps;
   static constexpr int pre_off = merge_off + merge_bytes;  // [1025] tiles before each sequence
   static constexpr int misc_off = pre_off + 1028 * 4;
-  static constexpr int misc_bytes = 3072;
+  static constexpr int misc_bytes = 3 * 1024;
   static constexpr int bytes = misc_off + misc_bytes + 1024;
   // two blocks per multiprocessor (228 KB, 1 KB of it reserved for each block)
   static_assert(2 * (bytes + 1024) <= 228 * 1024, "shared memory");
@@ -83,7 +83,7 @@ struct DecodeMisc {
   int abort;
   float q[128];
 };
-static_assert(sizeof(DecodeMisc) <= 3072, "misc");
+static_assert(sizeof(DecodeMisc) <= DecodeSmem<128, 1>::misc_bytes, "misc");
 static_assert(sizeof(LiteralScratch<kDecodeThreads, 128>) <= 8192, "it shares the merge buffer");
 
 struct DecodeMaps {
